@@ -1,4 +1,5 @@
-"""Build ``liblard.so`` (the C-ABI library) and ``liblard_probe.so`` for sm_100a with nvcc.
+"""Build ``liblard.so`` (the relation-KL C-ABI library), ``liblard_attn.so`` (the attention operators)
+and ``liblard_probe.so`` for sm_100a with nvcc.
 
 The library is built in-tree, next to this file, so that it travels with the
 repository.  cudart is linked statically: the library needs only the NVIDIA
@@ -12,6 +13,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 SRC_DIR = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "liblard.so")
+ATTN_LIB = os.path.join(HERE, "liblard_attn.so")
 PROBE_LIB = os.path.join(HERE, "liblard_probe.so")
 NVCC = os.environ.get("NVCC", "/usr/local/cuda/bin/nvcc")
 
@@ -20,15 +22,22 @@ FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std
          "-shared", "-cudart", "static"]
 
 # (library, main source, header) of each build target
-TARGETS = {"lard": (LIB, "lard.cu", "lard.h"), "probe": (PROBE_LIB, "lard_probe.cu", "lard_probe.h")}
+TARGETS = {"lard": (LIB, "lard.cu", "lard.h"), "attn": (ATTN_LIB, "lard_attn.cu", "lard_attn.h"),
+           "probe": (PROBE_LIB, "lard_probe.cu", "lard_probe.h")}
 
 
 def sources(target: str = "lard"):
-    """The files a target is built from: its main source, every kernel header and its C header."""
+    """The files a target is built from: its main source, every shared header, its C header,
+    and for the attention library the kernel headers of csrc/attn and the C header it extends."""
     _, main, header = TARGETS[target]
-    return ([os.path.join(SRC_DIR, main)] +
-            [os.path.join(SRC_DIR, f) for f in sorted(os.listdir(SRC_DIR)) if f.endswith(".cuh")] +
-            [os.path.join(ROOT, "include", header)])
+    files = ([os.path.join(SRC_DIR, main)] +
+             [os.path.join(SRC_DIR, f) for f in sorted(os.listdir(SRC_DIR)) if f.endswith((".cuh", ".h"))] +
+             [os.path.join(ROOT, "include", header)])
+    if target == "attn":
+        attn = os.path.join(SRC_DIR, "attn")
+        files += [os.path.join(attn, f) for f in sorted(os.listdir(attn)) if f.endswith(".cuh")]
+        files.append(os.path.join(ROOT, "include", "lard.h"))
+    return files
 
 
 def source_digest() -> str:
@@ -61,9 +70,10 @@ def build_target(target: str, force: bool = False, verbose_ptxas: bool = False) 
 
 
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Build liblard.so (the C-ABI library) and liblard_probe.so (the exponential-unit
-    probe the benchmark uses); returns the path of liblard.so."""
+    """Build liblard.so (the relation-KL library), liblard_attn.so (the attention operators) and
+    liblard_probe.so (the exponential-unit probe the benchmark uses); returns the path of liblard.so."""
     build_target("probe", force, verbose_ptxas)
+    build_target("attn", force, verbose_ptxas)
     return build_target("lard", force, verbose_ptxas)
 
 

@@ -3,7 +3,6 @@
 // of the relation-KL computation runs in the kernels of the included headers.
 #include <cuda.h>
 #include <cuda_runtime.h>
-#include <nvtx3/nvToolsExt.h>
 
 #include <climits>
 #include <cmath>
@@ -11,6 +10,7 @@
 #include <mutex>
 
 #include "lard.h"
+#include "lard_host.h"
 #include "lard_kernel_common.cuh"
 #include "lard_bwd_tc.cuh"
 #include "lard_cast.cuh"
@@ -24,11 +24,6 @@ constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s per wait
 constexpr unsigned long long kDrainLimitNs = 8000000000ull;  // 8 s per drain on the way out
 constexpr int kMaxDevices = 64;
 constexpr long long kMaxElems = 1LL << 40;
-
-using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
-                                   const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // Workspace of lard_kl_bwd_multi_bf16_noalloc, for callers that cannot
 // allocate device memory: a file-scope device array, present on every GPU
@@ -45,53 +40,9 @@ void* g_static_ws_ptr[kMaxDevices];
 lard_status g_dev_status[kMaxDevices];
 EncodeTiledFn g_encode = nullptr;
 
-// Restores the caller's current device when a call returns.
-struct DeviceGuard {
-    int prev = -1;
-    DeviceGuard() {
-        if (cudaGetDevice(&prev) != cudaSuccess) {
-            prev = -1;
-            cudaGetLastError();
-        }
-    }
-    ~DeviceGuard() {
-        if (prev >= 0) cudaSetDevice(prev);
-    }
-};
-
-// NVTX range over one call (a profiler that records NVTX shows each phase's
-// enqueue, and correlates the kernels it launched; without one it costs nothing).
-struct NvtxRange {
-    explicit NvtxRange(const char* name) { nvtxRangePushA(name); }
-    ~NvtxRange() { nvtxRangePop(); }
-};
-
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-bool overlap(const void* a, size_t na, const void* b, size_t nb) {
-    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-    return x < y + nb && y < x + na;
-}
-
 bool d_supported(lard_dtype dt, int d) {
     if (dt == LARD_DTYPE_BF16) return d == 64 || d == 128;
     return d >= 32 && d <= 256 && d % 32 == 0;
-}
-
-template <typename K>
-cudaError_t set_smem(K kernel, int bytes) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-}
-
-// The warp-specialised kernels move registers between warpgroups with
-// setmaxnreg; that only terminates if the block's launch allocation covers
-// every warpgroup's share.  Checks the built kernel's register count.
-template <typename K>
-bool split_fits(K kernel, int threads, int split_total) {
-    cudaFuncAttributes a;
-    if (cudaFuncGetAttributes(&a, kernel) != cudaSuccess) return false;
-    const int per_thread = (a.numRegs + 7) / 8 * 8;
-    return per_thread * threads >= split_total;
 }
 
 // One-time setup of device `dev` (made current by the caller).
@@ -106,14 +57,8 @@ lard_status setup_device(int dev) {
     lard_status st = LARD_OK;
     if (major != 10 || minor != 0) st = LARD_ERR_UNSUPPORTED;  // built for sm_100a only
     if (st == LARD_OK && !g_encode) {
-        void* fn = nullptr;
-        cudaDriverEntryPointQueryResult q;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault,
-                                             &q) != cudaSuccess ||
-            q != cudaDriverEntryPointSuccess || !fn)
-            st = LARD_ERR_CUDA;
-        else
-            g_encode = reinterpret_cast<EncodeTiledFn>(fn);
+        g_encode = find_encode_tiled();
+        if (!g_encode) st = LARD_ERR_CUDA;
     }
     if (st == LARD_OK) {
         bool ok = set_smem(lard::lard_fwd_tc_kernel<64>, lard::FwdLayout<64>::SMEM_BYTES) == cudaSuccess &&

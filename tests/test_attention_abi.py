@@ -1,0 +1,205 @@
+"""CPU checks of the attention library's C ABI: it exports what include/lard_attn.h declares
+and refuses bad arguments before any CUDA call (the addresses below are made up)."""
+import ctypes
+import os
+import re
+import subprocess
+import sys
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+HEADER = os.path.join(ROOT, "include", "lard_attn.h")
+
+
+class View(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("batch", ctypes.c_longlong), ("head", ctypes.c_longlong),
+                ("row", ctypes.c_longlong)]
+
+
+class Cross(ctypes.Structure):
+    _fields_ = ([(x, ctypes.c_int) for x in ("dtype", "B", "Hq", "Hkv", "n", "m", "d")] + [("tau", ctypes.c_float)] +
+                [(x, View) for x in "qkv"] + [("k_len", ctypes.c_void_p), ("out", View), ("lse", ctypes.c_void_p)] +
+                [(x, View) for x in ("dout", "dq", "dk", "dv")])
+
+
+class Prefix(ctypes.Structure):
+    _fields_ = ([(x, ctypes.c_int) for x in ("dtype", "B", "Hq", "Hkv", "n", "P", "S", "d")] + [("tau", ctypes.c_float)] +
+                [(x, View) for x in ("q", "kp", "vp", "ks", "vs")] +
+                [("s_len", ctypes.c_void_p), ("out", View), ("lse", ctypes.c_void_p)])
+
+
+@pytest.fixture(scope="module")
+def att():
+    from linear_memory_attention_b200 import build
+    build.build()
+    from linear_memory_attention_b200 import attention
+    return attention
+
+
+def test_exports_match_the_header(att):
+    text = open(HEADER).read()
+    names = re.findall(r"LARD_API\s+[\w\s\*]+?\b(lard_\w+)\s*\(", text)
+    assert set(names) == set(att.EXPORTS) and len(names) == len(set(names))
+    for name in names:
+        assert hasattr(att._lib, name)
+
+
+def test_packed_arguments_have_the_structs_layout(att):
+    assert att._CROSS.size == ctypes.sizeof(Cross) and att._PREFIX.size == ctypes.sizeof(Prefix)
+    c = Cross.from_buffer_copy(att._CROSS.pack(*range(7), 0.5, *range(8, 42)))
+    assert (c.d, c.tau, c.q.ptr, c.k.ptr, c.v.row, c.k_len, c.out.ptr, c.lse, c.dout.ptr, c.dv.row) == (
+        6, 0.5, 8, 12, 19, 20, 21, 25, 26, 41)
+    p = Prefix.from_buffer_copy(att._PREFIX.pack(*range(8), 0.5, *range(9, 35)))
+    assert (p.d, p.tau, p.q.ptr, p.kp.ptr, p.vs.row, p.s_len, p.out.ptr, p.lse) == (7, 0.5, 9, 13, 28, 29, 30, 34)
+
+
+def view(ptr, H, rows, d):
+    return View(ptr, H * rows * d, rows * d, d)
+
+
+STEP = 0x1000000  # more than any tensor here
+
+
+def cross_call(att, fn="fwd", ws=40 * STEP, ws_bytes=None, **kw):
+    """An in-order call on made-up addresses, changed by kw; returns the status."""
+    B, Hq, Hkv, n, m, d = (kw.pop(x, y) for x, y in (("B", 2), ("Hq", 4), ("Hkv", 2), ("n", 50), ("m", 70), ("d", 64)))
+    a = Cross(dtype=kw.pop("dtype", 0), B=B, Hq=Hq, Hkv=Hkv, n=n, m=m, d=d, tau=kw.pop("tau", 0.1), k_len=20 * STEP,
+              lse=21 * STEP)
+    for i, (x, H, rows) in enumerate((("q", Hq, n), ("k", Hkv, m), ("v", Hkv, m), ("out", Hq, n), ("dout", Hq, n),
+                                      ("dq", Hq, n), ("dk", Hkv, m), ("dv", Hkv, m))):
+        setattr(a, x, view((i + 1) * STEP, H, rows, d))
+    for x, y in kw.items():
+        if "_" in x and x != "k_len":
+            name, part = x.split("_")
+            setattr(getattr(a, name), part, y)
+        else:
+            setattr(a, x, y)
+    size = getattr(att._lib, f"lard_cross_attn_{fn}_workspace_bytes")(ctypes.byref(a))
+    return getattr(att._lib, f"lard_cross_attn_{fn}")(ctypes.byref(a), ws, size if ws_bytes is None else ws_bytes, None)
+
+
+def test_valid_arguments_reach_the_device_check(att):
+    """Without a GPU the calls below end there with LARD_ERR_CUDA, so that the refusals (1, 2)
+    are those of the argument checks; with one, the made-up addresses are refused there."""
+    end = 1 if torch.cuda.is_available() else 3
+    assert cross_call(att) == end and cross_call(att, "bwd") == end and prefix_call(att) == end
+    assert cross_call(att, k_batch=0, v_head=0) == end                 # inputs may be shared
+    assert cross_call(att, B=1, q_batch=7, out_batch=3) == end         # the stride of one element is not used
+    assert prefix_call(att, P=0, kp_ptr=None, vp_ptr=None) == end
+    assert prefix_call(att, S=0, ks_ptr=None, vs_ptr=None, s_len=1) == end
+    # dK and dV as the halves of one [B, m, 2, Hkv, d] buffer
+    halves = dict(dk_batch=70 * 256, dk_row=256, dk_head=64, dv_ptr=7 * STEP + 256, dv_batch=70 * 256, dv_row=256,
+                  dv_head=64)
+    assert cross_call(att, "bwd", **halves) == end
+    assert cross_call(att, "bwd", **dict(halves, dv_ptr=7 * STEP + 128)) == 1   # one head of each overlaps
+
+
+@pytest.mark.parametrize("kw", [
+    dict(B=0), dict(n=0), dict(m=0), dict(Hq=3), dict(Hkv=0), dict(tau=0.0), dict(tau=float("nan")),
+    dict(tau=float("inf")), dict(n=2 ** 31 - 1), dict(m=2 ** 31 - 1), dict(B=1 << 20, Hq=1 << 12), dict(q_ptr=None),
+    dict(k_ptr=2 * STEP + 8), dict(lse=None), dict(lse=21 * STEP + 2), dict(k_len=20 * STEP + 1), dict(q_row=66),
+    dict(q_row=32), dict(v_head=-64), dict(out_head=0), dict(out_batch=64), dict(out_row=60), dict(out_ptr=STEP),
+    dict(lse=STEP), dict(lse=4 * STEP), dict(k_len=21 * STEP), dict(q_batch=1 << 40),
+])
+def test_forward_refuses(att, kw):
+    assert cross_call(att, **kw) == 1
+
+
+@pytest.mark.parametrize("kw", [dict(d=32), dict(d=96), dict(d=256), dict(dtype=2), dict(dtype=-1)])
+def test_unsupported_types_and_head_sizes(att, kw):
+    assert cross_call(att, **kw) == 2 and cross_call(att, "bwd", **kw) == 2 and prefix_call(att, **kw) == 2
+
+
+@pytest.mark.parametrize("kw", [
+    dict(dq_ptr=None), dict(dk_ptr=8 * STEP), dict(dv_ptr=7 * STEP + 16), dict(dq_ptr=5 * STEP), dict(dout_ptr=None),
+    dict(dk_head=0), dict(out_ptr=None), dict(dv_ptr=2 * STEP), dict(lse=6 * STEP), dict(ws=40 * STEP + 4),
+    dict(ws=None), dict(ws_bytes=8), dict(ws=6 * STEP),
+])
+def test_backward_refuses(att, kw):
+    assert cross_call(att, "bwd", **kw) == 1
+
+
+def prefix_call(att, ws=40 * STEP, **kw):
+    B, Hq, Hkv, n, P, S, d = (kw.pop(x, y) for x, y in (("B", 2), ("Hq", 4), ("Hkv", 2), ("n", 3), ("P", 900), ("S", 70),
+                                                       ("d", 64)))
+    a = Prefix(dtype=kw.pop("dtype", 0), B=B, Hq=Hq, Hkv=Hkv, n=n, P=P, S=S, d=d, tau=kw.pop("tau", 0.1),
+               s_len=20 * STEP, lse=21 * STEP)
+    for i, (x, H, rows) in enumerate((("q", Hq, n), ("kp", Hkv, P), ("vp", Hkv, P), ("ks", Hkv, S), ("vs", Hkv, S),
+                                      ("out", Hq, n))):
+        setattr(a, x, view((i + 1) * STEP, H, rows, d))
+    for x, y in kw.items():
+        if "_" in x and x != "s_len":
+            name, part = x.split("_")
+            setattr(getattr(a, name), part, y)
+        else:
+            setattr(a, x, y)
+    size = att._lib.lard_prefix_attn_workspace_bytes(ctypes.byref(a))
+    return att._lib.lard_prefix_attn(ctypes.byref(a), ws, size, None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(P=-1), dict(S=-1), dict(P=0, S=0), dict(n=0), dict(Hq=5), dict(tau=-1.0), dict(kp_ptr=None), dict(vs_ptr=None),
+    dict(kp_row=65), dict(vp_head=-64), dict(ks_batch=4), dict(s_len=20 * STEP + 2), dict(out_ptr=STEP),
+    dict(lse=None), dict(ws=40 * STEP + 8), dict(ws=None), dict(ws=6 * STEP),
+])
+def test_prefix_refuses(att, kw):
+    assert prefix_call(att, **kw) == 1
+
+
+def test_null_arguments(att):
+    assert att._lib.lard_cross_attn_fwd(None, None, 0, None) == 1
+    assert att._lib.lard_cross_attn_bwd(None, None, 0, None) == 1
+    assert att._lib.lard_prefix_attn(None, None, 0, None) == 1
+    assert att._lib.lard_cross_attn_fwd_workspace_bytes(None) == 0
+    assert att._lib.lard_prefix_attn_workspace_bytes(None) == 0
+
+
+def test_binding_refuses(att):
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(s, dtype=dt)  # noqa: E731
+    q, k = z(2, 4, 5, 64), z(2, 2, 7, 64)
+    lse, out = z(2, 4, 5, dt=torch.float32), z(2, 4, 5, 64)
+    args = lambda **kw: att._cross_args(*[kw.get(x, y) for x, y in (  # noqa: E731
+        ("q", q), ("k", k), ("v", k), ("tau", 0.1), ("k_len", None), ("out", out), ("lse", lse))])
+    args()
+    for bad in (dict(q=q[0]), dict(k=k[0]), dict(v=z(2, 2, 8, 64)), dict(k=z(3, 2, 7, 64)), dict(k=z(2, 2, 7, 32)),
+                dict(q=q.half()), dict(k=k.float()), dict(out=out.float()), dict(lse=lse.double()), dict(lse=lse[:1]),
+                dict(k_len=z(2)), dict(k_len=z(3, dt=torch.int32)), dict(k_len=z(4, dt=torch.int32)[::2]),
+                dict(v=z(2, 2, 64, 7).transpose(2, 3)), dict(lse=z(2, 5, 4, dt=torch.float32).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            args(**bad)
+    with pytest.raises(ValueError):
+        att.lard_cross_attn_bwd(q, k, k, 0.1, out, lse, out, q, k, z(2, 2, 7, 64, dt=torch.float32))
+    with pytest.raises(ValueError):  # no workspace given where one is needed
+        att.lard_cross_attn_bwd(q, k, k, 0.1, out, lse, out, q, k, k)
+    with pytest.raises(ValueError):
+        att.lard_prefix_attn(q, None, None, None, None, None, 0.1, out, lse)
+    with pytest.raises(ValueError):
+        att.lard_prefix_attn(q, k[0], None, k, k, None, 0.1, out, lse)
+    with pytest.raises(ValueError):
+        att.lard_prefix_attn(q, z(3, 9, 64), z(3, 9, 64), k, k, None, 0.1, out, lse)
+    with pytest.raises(ValueError):
+        att.lard_prefix_attn(q, k, k, k, k, None, 0.1, out, lse)
+
+
+def test_workspace_grows_with_what_is_split(att):
+    """Few rows over many keys are split over blocks, whose partial rows need room; enough
+    rows need none."""
+    bf = torch.bfloat16
+    few, many = torch.empty((1, 8, 1, 128), dtype=bf), torch.empty((8, 32, 1, 128), dtype=bf).expand(8, 32, 4096, 128)
+    keys = torch.empty((1, 8, 1, 128), dtype=bf).expand(1, 8, 8000, 128)
+    assert att.lard_cross_attn_fwd_workspace_bytes(few, keys) >= 8 * 129 * 4
+    assert att.lard_cross_attn_fwd_workspace_bytes(many, keys.expand(8, 8, 8000, 128)) == 0
+
+
+def test_missing_library_is_an_import_error(tmp_path):
+    src = os.path.join(ROOT, "linear_memory_attention_b200")
+    pkg = tmp_path / "linear_memory_attention_b200"
+    pkg.mkdir()
+    for f in ("__init__.py", "lard.py", "attention.py"):
+        (pkg / f).write_text(open(os.path.join(src, f)).read())
+    os.symlink(os.path.join(src, "liblard.so"), pkg / "liblard.so")
+    out = subprocess.run([sys.executable, "-c", "import linear_memory_attention_b200.attention"], cwd=tmp_path,
+                         capture_output=True, text=True, timeout=300)
+    assert out.returncode != 0 and "ImportError" in out.stderr and "liblard_attn.so is not built" in out.stderr
