@@ -1,0 +1,492 @@
+// attn_fwd_tc.cuh -- the forward pass on the 5th-generation tensor cores (bf16).
+//
+// A block works on two streams at a time, so that the tensor pipe has one
+// stream's products while the other's exponentials are computed.  By rows
+// (kByKeys = 0): stream i owns the 128 query rows of its own tile, and both
+// read every key tile.  By keys (kByKeys = 1; at most 128 rows): both streams
+// own the same rows, stream i the key tiles 2t + i, and the two are joined at
+// the end.  Per stream and key tile of 128:
+//   S = Q K^T      A = Q (shared memory, K-major), B = K (K-major)
+//   P = 2^(S c - m), row sums in fp32, P rounded to bf16 over S's TMEM columns
+//   O += P V       A = P (TMEM), B = V (MN-major), O in TMEM
+// A row's reference m follows its maximum only when that has risen by more
+// than 2^8: P then stays below 2^8 and in bf16's relative precision whatever
+// m is, O and l are rescaled rarely, and the softmax threads do it themselves.
+// Per tile the tensor pipe needs 1024 cycles at d = 128 and the exponential
+// unit 1024 (128 * 128 / 16): both are near their limit, so a share of the
+// exponentials is computed on the FMA pipe.
+// Key tiles past a sequence's length are never visited.  Values of rows past
+// it inside the last tile are zeroed in shared memory before the product (0
+// times what is there could be NaN); their logits are replaced by -infinity.
+// TMEM (512 columns): S0 [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [384, 384 + D).
+// Roles (384 threads):
+//   warp 0       TMA producer of the K / V ring
+//   warp 1       TMEM owner, MMA issuer
+//   warps 4-11   one stream each warpgroup: Q rows into shared memory, softmax
+//                (one row a thread), the epilogue
+#pragma once
+
+#include "../lard_exp2.cuh"
+#include "attn_common.cuh"
+#include "attn_ptx.cuh"
+
+namespace lard {
+namespace attn {
+
+// Where a key segment lies for the TMA loads: maps {d, rows, heads, batch}.
+struct TcSeg {
+    CUtensorMap k, v;
+    const int* len;
+    int cap, causal;
+    int khead, kbatch, vhead, vbatch;  // 1, or 0 where one block is shared (stride 0)
+    __device__ __forceinline__ int length(int b) const {
+        if (!len) return cap;
+        const int l = len[b];
+        return l < 0 ? 0 : (l > cap ? cap : l);
+    }
+};
+
+// A launch: PB problems per key head, of R rows each; row r of problem pb is
+// sequence b = pb + r / (G n), query head hk G + r % (G n) / n, row r % n.
+// (Keys of their own: PB = B, R = G n.  Shared keys: PB = 1, R = B G n.)
+struct TcFwdArgs {
+    TcSeg seg[2];
+    View<const __nv_bfloat16> q;
+    View<__nv_bfloat16> out;
+    float* lse;  // [B, Hq, n]
+    int nseg, PB, Hkv, G, n, R;
+    int splits, split0;  // with join: partial rows go to split0 + split
+    int join;
+    long long rows;  // B Hkv G n
+    float* part_o;
+    float* part_lse;
+    float cfac;
+    unsigned long long wait_ns, drain_ns;
+};
+
+template <int D>
+struct FwdTcLayout {
+    static constexpr int KC = D / 64;
+    static constexpr int TILE = KC * 16384;
+    static constexpr int NS = D == 128 ? 5 : 10;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_CTRL = OFF_KV + NS * TILE;
+    static constexpr int SMEM_BYTES = OFF_CTRL + 2048 + 1024;
+    // By keys, the join stages a stream's O in the ring: 128 x D fp32.
+    static_assert(NS * TILE >= 128 * D * 4, "no room for the join");
+    static_assert(SMEM_BYTES <= 232448, "too much shared memory");
+};
+
+struct FwdTcCtrl {
+    uint64_t kv_full[10], kv_empty[10];
+    uint64_t q_ready, mma_done;
+    uint64_t s_full[2], p_full[2], o_full[2];
+    uint32_t tmem_base;
+    int abort_flag;
+    float join_m[128], join_l[128];
+};
+static_assert(sizeof(FwdTcCtrl) <= 2048, "control block too large");
+
+constexpr int kFwdTcThreads = 384;
+constexpr int kFwdTcRegsLaunch = 168, kFwdTcRegsCtl = 80, kFwdTcRegsSoft = 208;
+constexpr int kFwdTcRegsSplitTotal = 128 * (kFwdTcRegsCtl + 2 * kFwdTcRegsSoft);
+static_assert(kFwdTcRegsSplitTotal <= kFwdTcThreads * kFwdTcRegsLaunch, "register split exceeds the launch allocation");
+constexpr float kRiseLog2 = 8.0f;
+
+// Grid: row tiles (fastest), then splits, then PB * Hkv.
+template <int D, int kByKeys>
+__global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __grid_constant__ TcFwdArgs g) {
+    using L = FwdTcLayout<D>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
+    FwdTcCtrl* ctrl = reinterpret_cast<FwdTcCtrl*>(smem + L::OFF_CTRL);
+    volatile int* abort_flag = &ctrl->abort_flag;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    constexpr int kRowsPerBlock = kByKeys ? 128 : 256;
+    const int rtiles = (g.R + kRowsPerBlock - 1) / kRowsPerBlock;
+    const int r0 = static_cast<int>(blockIdx.x % rtiles) * kRowsPerBlock;
+    const int split = static_cast<int>(blockIdx.x / rtiles % g.splits);
+    const int ph = static_cast<int>(blockIdx.x / rtiles / g.splits);
+    const int pb = ph / g.Hkv, hk = ph % g.Hkv;
+
+    // This block's key tiles [t0, t0 + T) of the segments' tiles in a row.
+    const int len0 = g.seg[0].length(pb), len1 = g.nseg > 1 ? g.seg[1].length(pb) : 0;
+    const int tiles0 = (len0 + 127) / 128;
+    int t0, T;
+    {
+        const long long all = static_cast<long long>(tiles0) + (len1 + 127) / 128;
+        t0 = static_cast<int>(all * split / g.splits);
+        T = static_cast<int>(all * (split + 1) / g.splits) - t0;
+    }
+    // Streams and their steps: by rows each step is one tile for both, by keys two tiles.
+    const int nstream = kByKeys ? 2 : (g.R - r0 > 128 ? 2 : 1);
+    auto steps = [&](int i) { return kByKeys ? (T + 1 - i) / 2 : (i < nstream ? T : 0); };
+    const int S = steps(0);
+    auto tile_of = [&](int t, int i) { return t0 + (kByKeys ? 2 * t + i : t); };
+    // Segment and first key of a tile.
+    auto seg_of = [&](int tile) { return tile < tiles0 ? 0 : 1; };
+    auto key_of = [&](int tile) { return (tile < tiles0 ? tile : tile - tiles0) * 128; };
+    constexpr int kTiles = kByKeys ? 2 : 1;  // K (and V) tiles of a step
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < L::NS; ++s) {
+            ptx::mbar_init(&ctrl->kv_full[s], 1);
+            ptx::mbar_init(&ctrl->kv_empty[s], 1);
+        }
+        ptx::mbar_init(&ctrl->q_ready, 8);
+        ptx::mbar_init(&ctrl->mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&ctrl->s_full[i], 1);
+            ptx::mbar_init(&ctrl->p_full[i], 4);
+            ptx::mbar_init(&ctrl->o_full[i], 1);
+        }
+        ctrl->abort_flag = 0;
+        ptx::fence_mbar_init();
+    }
+    if (warp == 0 && lane == 0)
+        for (int s = 0; s < g.nseg; ++s) {
+            ptx::prefetch_tensormap(&g.seg[s].k);
+            ptx::prefetch_tensormap(&g.seg[s].v);
+        }
+    if (warp == 1) {
+        ptx::tmem_alloc(&ctrl->tmem_base, 512);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = ctrl->tmem_base;
+    const uint64_t lim = g.wait_ns, dlim = g.drain_ns;
+
+    if (warp < 4) {
+      ptx::regs_dec<kFwdTcRegsCtl>();
+      if (warp == 0) {
+        // ------------------------------------------------------------ producer
+        // Ring order: the K tiles of step 0, its V tiles, the K tiles of step 1, ...
+        int slot = 0, round = 0, issued = 0;
+        bool ok = true;
+        for (int t = 0; ok && t < S; ++t) {
+            for (int u = 0; ok && u < 2 * kTiles; ++u) {
+                const int i = u % kTiles;
+                const bool is_v = u >= kTiles;
+                if (kByKeys && t >= steps(i)) continue;
+                ok = ptx::mbar_wait(&ctrl->kv_empty[slot], (round & 1) ^ 1, abort_flag, lim, &g_lard_fault,
+                                    kFaultFwdProducer);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                if (lane == 0) {
+                    const int tile = tile_of(t, i);
+                    const TcSeg& seg = g.seg[seg_of(tile)];
+                    uint8_t* dst = smem + L::OFF_KV + slot * L::TILE;
+                    ptx::mbar_arrive_expect_tx(&ctrl->kv_full[slot], L::TILE);
+                    for (int c = 0; c < L::KC; ++c)
+                        tma_load_4d(dst + c * 16384, is_v ? &seg.v : &seg.k, &ctrl->kv_full[slot], c * 64,
+                                    key_of(tile), (is_v ? seg.vhead : seg.khead) ? hk : 0,
+                                    (is_v ? seg.vbatch : seg.kbatch) ? pb : 0);
+                }
+                __syncwarp();
+                ++issued;
+                if (++slot == L::NS) { slot = 0; ++round; }
+            }
+        }
+        // Let every copy this warp started land before the block can exit.
+        for (int s = 0; s < L::NS && s < issued; ++s) {
+            const int last = s + L::NS * ((issued - 1 - s) / L::NS);
+            drain(&ctrl->kv_full[s], (last / L::NS) & 1, dlim);
+        }
+      } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer
+        constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
+        constexpr uint32_t kIdescO = ptx::idesc_bf16(128, D, 0, 1);
+        constexpr uint32_t kHi = ptx::sdesc_hi(1024);
+        const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_Q), 16);
+        const uint32_t kv_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16);
+        const uint32_t kv_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16384);
+        // Ring slot of a step's K or V tile; all steps but the last have 2 * kTiles slots.
+        auto index_of = [&](int t, int u) {
+            if (kByKeys && t == S - 1 && steps(1) < S) return 4 * t + (u >= 2 ? 1 : 0);
+            return 2 * kTiles * t + u;
+        };
+        auto wait_slot = [&](int idx) {
+            const bool ok = ptx::mbar_wait(&ctrl->kv_full[idx % L::NS], (idx / L::NS) & 1, abort_flag, lim,
+                                           &g_lard_fault, kFaultFwdMma);
+            return __all_sync(0xffffffffu, ok) != 0;
+        };
+        auto issue_s = [&](int i, int idx) {  // S_i = Q_i K^T; Q is one tile by keys
+            const uint32_t a = q_lo + (kByKeys ? 0 : i * (L::TILE >> 4)), b = kv_k + (idx % L::NS) * (L::TILE >> 4);
+            const uint32_t d = tmem + i * 128;
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+                if (kk == 0) ptx::umma_ss<0>(d, a, b, kHi, kIdescS);
+                else ptx::umma_ss<1>(d, a + ptx::desc_step_k(kk), b + ptx::desc_step_k(kk), kHi, kIdescS);
+            }
+            ptx::umma_commit(&ctrl->s_full[i]);
+        };
+        auto issue_o = [&](int i, int idx, bool first) {  // O_i (+)= P_i V
+            const uint32_t a = tmem + i * 128, b = kv_mn + (idx % L::NS) * (L::TILE >> 4);
+            const uint32_t d = tmem + 256 + i * 128;
+            umma_ts_acc(d, a, b, kHi, kIdescO, first ? 0u : 1u);
+#pragma unroll
+            for (int kk = 1; kk < 8; ++kk) ptx::umma_ts<1>(d, a + kk * 8, b + ptx::desc_step_mn(kk), kHi, kIdescO);
+            ptx::umma_commit(&ctrl->o_full[i]);
+        };
+        bool ok = S > 0 && ptx::mbar_wait(&ctrl->q_ready, 0, abort_flag, lim, &g_lard_fault, kFaultFwdMma);
+        ok = __all_sync(0xffffffffu, ok);
+        if (ok) ptx::tc_fence_after();
+        for (int i = 0; ok && i < nstream; ++i) {
+            if (steps(i) == 0) continue;
+            const int ik = index_of(0, kByKeys ? i : 0);
+            ok = wait_slot(ik);
+            if (!ok) break;
+            if (lane == 0) {
+                issue_s(i, ik);
+                if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[ik % L::NS]);
+            }
+            __syncwarp();
+        }
+        for (int t = 0; ok && t < S; ++t) {
+            for (int i = 0; ok && i < nstream; ++i) {
+                if (t >= steps(i)) continue;
+                const int iv = index_of(t, kTiles + (kByKeys ? i : 0));
+                if (kByKeys || i == 0) {
+                    ok = wait_slot(iv);
+                    if (!ok) break;
+                    // Rows past the sequence's end inside its last tile.
+                    const int tile = tile_of(t, i);
+                    const int valid = (seg_of(tile) ? len1 : len0) - key_of(tile);
+                    if (valid < 128) {
+                        uint8_t* v = smem + L::OFF_KV + (iv % L::NS) * L::TILE;
+                        for (int e = valid * 8 + lane; e < 1024; e += 32)
+                            for (int c = 0; c < L::KC; ++c)
+                                *reinterpret_cast<uint4*>(v + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        ptx::fence_proxy_async_smem();
+                        __syncwarp();
+                    }
+                }
+                ok = ptx::mbar_wait(&ctrl->p_full[i], t & 1, abort_flag, lim, &g_lard_fault, kFaultFwdMma);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                if (lane == 0) {
+                    issue_o(i, iv, t == 0);
+                    if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[iv % L::NS]);
+                }
+                __syncwarp();
+                if (t + 1 < steps(i)) {  // behind O_i, whose P lies where S_i goes
+                    const int ik = index_of(t + 1, kByKeys ? i : 0);
+                    if (kByKeys || i == 0) {
+                        ok = wait_slot(ik);
+                        if (!ok) break;
+                    }
+                    if (lane == 0) {
+                        issue_s(i, ik);
+                        if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[ik % L::NS]);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) ptx::umma_commit(&ctrl->mma_done);
+        __syncwarp();
+        drain(&ctrl->mma_done, 0, dlim);
+      }
+    } else {
+        ptx::regs_inc<kFwdTcRegsSoft>();
+        // ------------------------------------------------------------ softmax
+        const int q4 = warp & 3;
+        const int i = (warp - 4) >> 2;  // stream
+        const int row = q4 * 32 + lane;
+        const int r = r0 + (kByKeys ? 0 : i * 128) + row;
+        const bool row_ok = r < g.R;
+        const int Gn = g.G * g.n;
+        const int b = pb + (row_ok ? r / Gn : 0), rem = row_ok ? r % Gn : 0;
+        const int head = hk * g.G + rem / g.n, pos = rem % g.n;
+        // Q into shared memory, rows past the end as zeros; by keys each
+        // stream writes half of the one tile's columns.
+        {
+            const uint4* src = reinterpret_cast<const uint4*>(g.q.row(b, head, pos));
+            const uint32_t dst = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE) + row * 128;
+            constexpr int kUnits = D / 8;
+#pragma unroll
+            for (int e = 0; e < (kByKeys ? kUnits / 2 : kUnits); ++e) {
+                const int u = kByKeys ? i * (kUnits / 2) + e : e;
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (row_ok) x = __ldg(src + u);
+                ptx::st_shared_v4(dst + (u >> 3) * 16384 + (((u & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
+            }
+            ptx::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctrl->q_ready);
+        }
+        const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
+        const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
+        const float cf = g.cfac;
+        float m = -INFINITY, l = 0.f;  // reference (log2 domain) and sum of 2^(z - m)
+        const int mine = steps(i);
+        bool ok = true;
+        for (int t = 0; t < mine; ++t) {
+            const int tile = tile_of(t, i), s = seg_of(tile), j0 = key_of(tile);
+            const int size = s ? len1 : len0;
+            const int lim_keys = (g.seg[s].causal ? causal_limit(size, g.n, pos) : size) - j0;
+            ok = ptx::mbar_wait(&ctrl->s_full[i], t & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) break;
+            ptx::tc_fence_after();
+            float z[4][32];
+            __syncwarp();
+#pragma unroll
+            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, z[c]);
+            ptx::tmem_ld_wait(z[0]);
+#pragma unroll
+            for (int c = 1; c < 4; ++c) ptx::reg_dep(z[c]);
+            if (lim_keys < 128) {
+#pragma unroll
+                for (int c = 0; c < 128; ++c)
+                    if (c >= lim_keys) z[c >> 5][c & 31] = -INFINITY;
+            }
+            float top[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                top[c] = fmaxf(z[c][0], z[c][1]);
+#pragma unroll
+                for (int k = 2; k < 32; k += 2) top[c] = ptx::fmax3(top[c], z[c][k], z[c][k + 1]);
+            }
+            const float mx = fmaxf(ptx::fmax3(top[0], top[1], top[2]), top[3]) * cf;
+            const bool rise = mx > m + kRiseLog2;  // always where the row has seen nothing yet and now does
+            const float mnew = rise ? mx : m;
+            if (__any_sync(0xffffffffu, rise) && t > 0) {
+                // O(t - 1) is complete; bring it to the new reference.
+                const float sc = rise ? ptx::ex2(m - mnew) : 1.f;
+                l *= sc;
+                ok = ptx::mbar_wait(&ctrl->o_full[i], (t - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    ptx::tmem_ld32(to + c, o);
+                    ptx::tmem_ld_wait(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= sc;
+                    ptx::tmem_st32(to + c, reinterpret_cast<const uint32_t(&)[32]>(o));
+                    ptx::tmem_st_wait();
+                }
+            }
+            m = mnew;
+            const float base = m == -INFINITY ? 0.f : m;  // nothing seen yet: every exponential below is 0
+            const float2 cf2 = splat2(cf), nb2 = splat2(-base);
+            float2 sum = splat2(0.f);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t pk[32];
+#pragma unroll
+                for (int k = 0; k < 64; k += 2) {
+                    const int c = h * 64 + k;
+                    const float2 u = fma2(make_float2(z[c >> 5][c & 31], z[c >> 5][(c & 31) + 1]), cf2, nb2);
+                    const float2 p = make_float2(ptx::ex2(u.x), ptx::ex2(u.y));
+                    sum = add2(sum, p);
+                    pk[k >> 1] = ptx::pack_bf16x2(p.x, p.y);
+                }
+                __syncwarp();
+                ptx::tmem_st32(ts + h * 32, pk);
+            }
+            ptx::tmem_st_wait();
+            l += sum.x + sum.y;
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctrl->p_full[i]);
+        }
+        // ------------------------------------------------------------ epilogue
+        if (ok && mine > 0) {
+            ok = ptx::mbar_wait(&ctrl->o_full[i], (mine - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+            ok = __all_sync(0xffffffffu, ok);
+            ptx::tc_fence_after();
+        }
+        float* stage = reinterpret_cast<float*>(smem + L::OFF_KV);  // [D][128], the ring is empty by then
+        float w0 = 1.f, w1 = 0.f, m_all = m, l_all = l;
+        if (kByKeys) {
+            // Stream 1 leaves its rows, stream 0 joins them to its own.  Stream 1's
+            // last product is the ring's last reader but for stream 0's, whose
+            // threads wait for theirs before the first barrier.
+            ptx::named_bar_sync(1, 256);
+            if (i == 1) {
+                ctrl->join_m[row] = m;
+                ctrl->join_l[row] = l;
+                if (ok && mine > 0) {
+#pragma unroll
+                    for (int c = 0; c < D; c += 32) {
+                        float o[32];
+                        __syncwarp();
+                        ptx::tmem_ld32(to + c, o);
+                        ptx::tmem_ld_wait(o);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) stage[(c + k) * 128 + row] = o[k];
+                    }
+                }
+            }
+            ptx::named_bar_sync(1, 256);
+            if (i == 0) {
+                const float m1 = ctrl->join_m[row];
+                m_all = fmaxf(m, m1);
+                const float base = m_all == -INFINITY ? 0.f : m_all;
+                w0 = ptx::ex2(m - base);
+                w1 = ptx::ex2(m1 - base);
+                l_all = l * w0 + ctrl->join_l[row] * w1;
+            }
+        }
+        if (ok && !*abort_flag && (!kByKeys || i == 0)) {
+            const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
+            w0 *= inv;
+            w1 *= inv;
+            const float lse = l_all == 0.f ? -INFINITY : (m_all + log2f(l_all)) * kLn2;
+            const long long grow = (static_cast<long long>(b) * g.Hkv + hk) * Gn + rem;
+            const long long prow = (g.split0 + split) * g.rows + grow;
+            const bool second = kByKeys && steps(1) > 0;
+#pragma unroll
+            for (int c = 0; c < D; c += 32) {
+                float o[32];
+                __syncwarp();
+                if (mine > 0) {
+                    ptx::tmem_ld32(to + c, o);
+                    ptx::tmem_ld_wait(o);
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] *= w0;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                }
+                if (second) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(c + k) * 128 + row], w1, o[k]);
+                }
+                if (row_ok && g.join) {
+                    float* dst = g.part_o + prow * D + c;
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) store4(dst + k, make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
+                } else if (row_ok) {
+                    uint4* dst = reinterpret_cast<uint4*>(g.out.row(b, head, pos) + c);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(ptx::pack_bf16x2(o[8 * k], o[8 * k + 1]), ptx::pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
+                                            ptx::pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), ptx::pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                }
+            }
+            if (row_ok) {
+                if (g.join) g.part_lse[prow] = lse;
+                else g.lse[grow] = lse;
+            }
+        }
+    }
+
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+}
+
+}  // namespace attn
+}  // namespace lard

@@ -8,11 +8,13 @@
 #include <cmath>
 #include <cstdint>
 #include <mutex>
+#include <type_traits>
 
 #include "lard_attn.h"
 #include "lard_host.h"
 #include "lard_kernel_common.cuh"
 #include "attn/attn_common.cuh"
+#include "attn/attn_fwd_tc.cuh"
 #include "attn/attn_simt.cuh"
 
 namespace {
@@ -23,6 +25,8 @@ using lard::attn::KeySeg;
 using lard::attn::View;
 using bf16 = __nv_bfloat16;
 
+constexpr unsigned long long kWaitLimitNs = 2000000000ull;   // 2 s per wait
+constexpr unsigned long long kDrainLimitNs = 8000000000ull;  // 8 s per drain on the way out
 constexpr int kMaxDevices = 64;
 constexpr int kSms = 148;  // of a B200: plans depend on sizes alone, so that a workspace can be sized without a GPU
 constexpr int kMaxRows = INT_MAX - 255;
@@ -30,6 +34,7 @@ constexpr int kMaxRows = INT_MAX - 255;
 std::mutex g_mu;
 bool g_ready[kMaxDevices];
 lard_status g_dev_status[kMaxDevices];
+EncodeTiledFn g_encode = nullptr;
 
 // One-time setup of device `dev` (made current by the caller).
 lard_status setup_device(int dev) {
@@ -42,14 +47,27 @@ lard_status setup_device(int dev) {
         return LARD_ERR_CUDA;
     lard_status st = LARD_OK;
     if (major != 10 || minor != 0) st = LARD_ERR_UNSUPPORTED;  // built for sm_100a only
+    if (st == LARD_OK && !g_encode) {
+        g_encode = find_encode_tiled();
+        if (!g_encode) st = LARD_ERR_CUDA;
+    }
     if (st == LARD_OK) {
         using namespace lard::attn;
-        bool ok = true;
+        bool ok = true, fits = true;
+        auto fwd_tc = [&](auto kernel, int smem) {
+            ok = ok && set_smem(kernel, smem) == cudaSuccess;
+            fits = fits && split_fits(kernel, kFwdTcThreads, kFwdTcRegsSplitTotal);
+        };
+        fwd_tc(attn_fwd_tc_kernel<64, 0>, FwdTcLayout<64>::SMEM_BYTES);
+        fwd_tc(attn_fwd_tc_kernel<64, 1>, FwdTcLayout<64>::SMEM_BYTES);
+        fwd_tc(attn_fwd_tc_kernel<128, 0>, FwdTcLayout<128>::SMEM_BYTES);
+        fwd_tc(attn_fwd_tc_kernel<128, 1>, FwdTcLayout<128>::SMEM_BYTES);
         auto simt = [&](auto t, auto d) {
             using T = decltype(t);
             constexpr int D = decltype(d)::value;
-            ok = ok && set_smem(attn_fwd_simt_kernel<T, D>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
-                 set_smem(attn_dkdv_simt_kernel<T, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess &&
+            if constexpr (std::is_same<T, float>::value)
+                ok = ok && set_smem(attn_fwd_simt_kernel<T, D>, SimtLayout<D>::FWD_BYTES) == cudaSuccess;
+            ok = ok && set_smem(attn_dkdv_simt_kernel<T, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess &&
                  set_smem(attn_dq_simt_kernel<T, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess;
         };
         simt(float(), std::integral_constant<int, 64>());
@@ -57,6 +75,7 @@ lard_status setup_device(int dev) {
         simt(bf16(), std::integral_constant<int, 64>());
         simt(bf16(), std::integral_constant<int, 128>());
         if (!ok) st = LARD_ERR_CUDA;
+        else if (!fits) st = LARD_ERR_UNSUPPORTED;  // a build whose register count cannot host the split
     }
     g_dev_status[dev] = st;
     g_ready[dev] = true;
@@ -189,47 +208,256 @@ View<T> view(const lard_attn_view& v) {
 }
 
 // ------------------------------------------------------------------ forward
-// How a forward pass over `keys` keys at most (two segments' tiles) is laid out.
-struct FwdPlan {
-    long long rtiles, blocks, rows;
-    int splits;
-    size_t part_o, part_lse;  // bytes
-    size_t bytes() const { return part_o + part_lse; }
+constexpr long long kJoinRowsPerBlock = 8;
+
+long long tiles_of(long long rows, int tile) { return (rows + tile - 1) / tile; }
+
+// One pass over the keys of a call: PB problems per key head of R rows each
+// over at most `tiles` key tiles, the key axis dealt to `splits` blocks.
+struct Pass {
+    long long blocks = 0;
+    int splits = 0, by_keys = 0;
 };
 
-FwdPlan plan_fwd(long long BH, long long R, int d, long long key_tiles) {
-    FwdPlan p;
-    p.rows = BH * R;
-    p.rtiles = (R + lard::attn::kSimtTile - 1) / lard::attn::kSimtTile;
-    p.blocks = BH * p.rtiles;
-    // Fewer blocks than SMs: the key tiles of each are dealt to several blocks, two an SM in all.
-    long long splits = 1;
-    if (p.blocks < kSms) splits = std::max(1LL, std::min(key_tiles, 2 * kSms / p.blocks));
-    p.splits = static_cast<int>(splits);
-    p.part_o = splits > 1 ? static_cast<size_t>(splits) * p.rows * d * 4 : 0;
-    p.part_lse = splits > 1 ? (static_cast<size_t>(splits) * p.rows * 4 + 15) / 16 * 16 : 0;
+// A forward call: one pass, or two (prefix attention: the shared keys, then
+// each sequence's own), and what they leave for the join.
+struct FwdPlan {
+    Pass pass[2];
+    int npass = 0;
+    long long rows = 0;  // of the whole call
+    int d = 0;
+    int partials() const { return pass[0].splits + pass[1].splits; }
+    bool join() const { return partials() > 1; }
+    size_t part_o() const { return join() ? static_cast<size_t>(partials()) * rows * d * 4 : 0; }
+    size_t part_lse() const { return join() ? (static_cast<size_t>(partials()) * rows * 4 + 15) / 16 * 16 : 0; }
+    size_t bytes() const { return part_o() + part_lse(); }
+    bool grids_fit() const {
+        for (int k = 0; k < npass; ++k)
+            if (pass[k].blocks * pass[k].splits > INT_MAX) return false;
+        return tiles_of(rows, kJoinRowsPerBlock) <= INT_MAX;
+    }
+};
+
+// CUDA-core pass: fewer blocks than SMs have the key tiles of each dealt to
+// several blocks, two an SM in all.
+Pass plan_simt(long long problems, long long R, long long tiles) {
+    Pass p;
+    p.blocks = problems * tiles_of(R, lard::attn::kSimtTile);
+    p.splits = 1;
+    if (p.blocks < kSms) p.splits = static_cast<int>(std::max(1LL, std::min(tiles, 2 * kSms / p.blocks)));
     return p;
 }
 
+// Tensor-core pass.  Up to 128 rows the two streams of a block share them and
+// take alternate key tiles; more rows take one tile of rows each.  The number
+// of splits is the one that a model of the pass's time gives, in cycles: a
+// step (two tiles' products and exponentials) takes about 2200, a block's
+// prologue and epilogue 6000, the join 8000 and its bytes; one step of a pass
+// that reads each key tile once cannot be faster than HBM (3400 B a cycle)
+// brings the tiles of all running blocks.
+Pass plan_tc(long long problems, long long R, int d, long long tiles, long long rows) {
+    Pass p;
+    p.by_keys = R <= 128;
+    const long long rtiles = tiles_of(R, p.by_keys ? 128 : 256);
+    p.blocks = problems * rtiles;
+    double best = 0.0;
+    const long long most = std::max(1LL, std::min(64LL, p.by_keys ? tiles / 2 : tiles));
+    for (long long s = 1; s <= most; ++s) {
+        const long long waves = tiles_of(p.blocks * s, kSms), running = std::min<long long>(kSms, p.blocks * s);
+        const double steps = static_cast<double>(tiles_of(tiles_of(tiles, s), p.by_keys ? 2 : 1));
+        double step = 2200.0;
+        if (rtiles == 1) step = std::max(step, (p.by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
+        double cost = waves * (steps * step + 6000.0);
+        if (s > 1) cost += 8000.0 + 8.0 * s * rows * d / 3400.0;
+        if (s == 1 || cost < best) {
+            best = cost;
+            p.splits = static_cast<int>(s);
+        }
+    }
+    return p;
+}
+
+// The forward work of a call, whatever its type: the views and the key segments.
+struct Fwd {
+    lard_dtype dtype;
+    int B, Hq, Hkv, n, d;
+    float tau;
+    lard_attn_view q, out;
+    float* lse;
+    struct Seg {
+        lard_attn_view k, v;
+        int rows;
+        const int* len;
+        int shared, causal;  // shared: one block of keys for all sequences
+    } seg[2];
+    int nseg;
+    long long group_rows() const { return static_cast<long long>(Hq / Hkv) * n; }
+};
+
+FwdPlan plan_fwd(const Fwd& f) {
+    FwdPlan p;
+    p.d = f.d;
+    p.rows = static_cast<long long>(f.B) * f.Hkv * f.group_rows();
+    const long long own = static_cast<long long>(f.B) * f.Hkv;
+    if (f.dtype == LARD_DTYPE_FP32) {
+        long long tiles = 0;
+        for (int s = 0; s < f.nseg; ++s) tiles += tiles_of(f.seg[s].rows, lard::attn::kSimtTile);
+        p.pass[p.npass++] = plan_simt(own, f.group_rows(), tiles);
+        return p;
+    }
+    for (int s = 0; s < f.nseg; ++s) {
+        const bool shared = f.seg[s].shared;
+        p.pass[p.npass++] = plan_tc(shared ? f.Hkv : own, f.group_rows() * (shared ? f.B : 1), f.d,
+                                    tiles_of(f.seg[s].rows, 128), p.rows);
+    }
+    return p;
+}
+
+// 4-D tensor map of a K or V tensor with 64 x 128 boxes, 128-byte swizzle; rows
+// past the end read as zeros.  A dimension of one element, or of one block for all
+// (stride 0), has one entry.
+bool make_kv_map(CUtensorMap* m, const lard_attn_view& v, long long B, long long H, long long rows, int d) {
+    const cuuint64_t line = static_cast<cuuint64_t>(d) * 2;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
+                          static_cast<cuuint64_t>(v.head ? H : 1), static_cast<cuuint64_t>(v.batch ? B : 1)};
+    cuuint64_t strides[3] = {v.row ? static_cast<cuuint64_t>(v.row) * 2 : line,
+                             v.head ? static_cast<cuuint64_t>(v.head) * 2 : line,
+                             v.batch ? static_cast<cuuint64_t>(v.batch) * 2 : line};
+    cuuint32_t box[4] = {64, 128, 1, 1};
+    cuuint32_t estr[4] = {1, 1, 1, 1};
+    return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+float log2_factor(float tau) { return static_cast<float>(static_cast<double>(tau) * 1.4426950408889634); }
+
+template <typename T>
+FwdArgs<T> fwd_args(const Fwd& f) {
+    FwdArgs<T> g;
+    g.q = view<const T>(f.q);
+    g.out = view<T>(f.out);
+    g.lse = f.lse;
+    for (int s = 0; s < 2; ++s) {
+        const Fwd::Seg& x = f.seg[s < f.nseg ? s : 0];
+        g.seg[s] = KeySeg<T>{view<const T>(x.k), view<const T>(x.v), x.len, x.rows, x.causal};
+    }
+    g.nseg = f.nseg;
+    g.B = f.B;
+    g.Hkv = f.Hkv;
+    g.G = f.Hq / f.Hkv;
+    g.n = f.n;
+    g.cfac = log2_factor(f.tau);
+    return g;
+}
+
 template <typename T, int D>
-void launch_fwd(FwdArgs<T>& g, const FwdPlan& p, void* ws, cudaStream_t s) {
+lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t stream) {
     using namespace lard::attn;
-    g.splits = p.splits;
+    FwdArgs<T> g = fwd_args<T>(f);
+    g.splits = p.partials();
     g.part_o = static_cast<float*>(ws);
-    g.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_o);
-    attn_fwd_simt_kernel<T, D><<<static_cast<unsigned>(p.blocks * p.splits), kSimtThreads, SimtLayout<D>::FWD_BYTES, s>>>(g);
-    if (p.splits > 1) attn_join_kernel<T, D><<<static_cast<unsigned>((p.rows + 7) / 8), 256, 0, s>>>(g);
+    g.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_o());
+    if constexpr (std::is_same<T, float>::value) {
+        attn_fwd_simt_kernel<T, D>
+            <<<static_cast<unsigned>(p.pass[0].blocks * p.pass[0].splits), kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(g);
+    } else {
+        TcFwdArgs a;
+        a.q = g.q;
+        a.out = g.out;
+        a.lse = g.lse;
+        a.nseg = 1;
+        a.Hkv = g.Hkv;
+        a.G = g.G;
+        a.n = g.n;
+        a.join = p.join();
+        a.rows = p.rows;
+        a.part_o = g.part_o;
+        a.part_lse = g.part_lse;
+        a.cfac = g.cfac;
+        a.wait_ns = kWaitLimitNs;
+        a.drain_ns = kDrainLimitNs;
+        a.split0 = 0;
+        for (int k = 0; k < p.npass; ++k) {
+            const Fwd::Seg& x = f.seg[k];
+            TcSeg& s = a.seg[0];
+            if (!make_kv_map(&s.k, x.k, x.shared ? 1 : f.B, f.Hkv, x.rows, D) ||
+                !make_kv_map(&s.v, x.v, x.shared ? 1 : f.B, f.Hkv, x.rows, D))
+                return LARD_ERR_INVALID_ARG;
+            s.len = x.len;
+            s.cap = x.rows;
+            s.causal = x.causal;
+            s.khead = x.k.head != 0;
+            s.kbatch = x.k.batch != 0;
+            s.vhead = x.v.head != 0;
+            s.vbatch = x.v.batch != 0;
+            a.seg[1] = s;
+            a.PB = x.shared ? 1 : f.B;
+            a.R = static_cast<int>(f.group_rows() * (x.shared ? f.B : 1));
+            a.splits = p.pass[k].splits;
+            const unsigned grid = static_cast<unsigned>(p.pass[k].blocks * p.pass[k].splits);
+            if (p.pass[k].by_keys)
+                attn_fwd_tc_kernel<D, 1><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
+            else
+                attn_fwd_tc_kernel<D, 0><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
+            a.split0 += p.pass[k].splits;
+        }
+    }
+    if (p.join())
+        attn_join_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.rows, kJoinRowsPerBlock)), 256, 0, stream>>>(g);
+    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
 }
 
-long long key_tiles(int rows) { return (static_cast<long long>(rows) + lard::attn::kSimtTile - 1) / lard::attn::kSimtTile; }
-
-FwdPlan cross_plan(const lard_cross_attn& a) {
-    return plan_fwd(static_cast<long long>(a.B) * a.Hkv, static_cast<long long>(a.Hq / a.Hkv) * a.n, a.d, key_tiles(a.m));
+Fwd cross_work(const lard_cross_attn& a, const lard_attn_view* v = nullptr) {
+    Fwd f{};
+    f.dtype = a.dtype;
+    f.B = a.B;
+    f.Hq = a.Hq;
+    f.Hkv = a.Hkv;
+    f.n = a.n;
+    f.d = a.d;
+    f.tau = a.tau;
+    f.lse = a.lse;
+    f.nseg = 1;
+    f.seg[0].rows = a.m;
+    f.seg[0].len = a.k_len;
+    if (v) {
+        f.q = v[0];
+        f.seg[0].k = v[1];
+        f.seg[0].v = v[2];
+        f.out = v[3];
+    }
+    return f;
 }
 
-FwdPlan prefix_plan(const lard_prefix_attn_args& a) {
-    return plan_fwd(static_cast<long long>(a.B) * a.Hkv, static_cast<long long>(a.Hq / a.Hkv) * a.n, a.d,
-                    key_tiles(a.P) + key_tiles(a.S));
+Fwd prefix_work(const lard_prefix_attn_args& a, const lard_attn_view* v = nullptr) {
+    Fwd f{};
+    f.dtype = a.dtype;
+    f.B = a.B;
+    f.Hq = a.Hq;
+    f.Hkv = a.Hkv;
+    f.n = a.n;
+    f.d = a.d;
+    f.tau = a.tau;
+    f.lse = a.lse;
+    if (v) {
+        f.q = v[0];
+        f.out = v[5];
+    }
+    for (int own = 0; own < 2; ++own) {
+        const int rows = own ? a.S : a.P;
+        if (rows == 0) continue;
+        Fwd::Seg& s = f.seg[f.nseg++];
+        s.rows = rows;
+        s.len = own ? a.s_len : nullptr;
+        s.shared = !own;
+        s.causal = own;
+        if (v) {
+            s.k = v[1 + 2 * own];
+            s.v = v[2 + 2 * own];
+        }
+    }
+    return f;
 }
 
 lard_status cross_sizes(const lard_cross_attn* a) {
@@ -237,9 +465,8 @@ lard_status cross_sizes(const lard_cross_attn* a) {
     lard_status st = check_sizes(a->dtype, a->B, a->Hq, a->Hkv, a->n, a->d, a->tau);
     if (st != LARD_OK) return st;
     if (a->m < 1 || a->m > kMaxRows) return LARD_ERR_INVALID_ARG;
-    const FwdPlan p = cross_plan(*a);
-    if (p.blocks * p.splits > INT_MAX || (p.rows + 7) / 8 > INT_MAX ||
-        static_cast<long long>(a->B) * a->Hkv * key_tiles(a->m) > INT_MAX)
+    if (!plan_fwd(cross_work(*a)).grids_fit() ||
+        static_cast<long long>(a->B) * a->Hkv * tiles_of(a->m, lard::attn::kSimtTile) > INT_MAX)
         return LARD_ERR_INVALID_ARG;
     return LARD_OK;
 }
@@ -250,48 +477,18 @@ lard_status prefix_sizes(const lard_prefix_attn_args* a) {
     if (st != LARD_OK) return st;
     if (a->P < 0 || a->S < 0 || (a->P == 0 && a->S == 0) || a->P > kMaxRows || a->S > kMaxRows)
         return LARD_ERR_INVALID_ARG;
-    const FwdPlan p = prefix_plan(*a);
-    if (p.blocks * p.splits > INT_MAX || (p.rows + 7) / 8 > INT_MAX) return LARD_ERR_INVALID_ARG;
-    return LARD_OK;
+    if (static_cast<long long>(a->B) * (a->Hq / a->Hkv) * a->n > kMaxRows) return LARD_ERR_INVALID_ARG;
+    return plan_fwd(prefix_work(*a)).grids_fit() ? LARD_OK : LARD_ERR_INVALID_ARG;
 }
 
 bool workspace_ok(const void* ws, size_t have, size_t need) {
     return need == 0 || (ws && aligned(ws, 16) && have >= need);
 }
 
-template <typename T, int D>
-void cross_fwd(const lard_cross_attn& a, const lard_attn_view (&v)[4], void* ws, cudaStream_t stream) {
-    FwdArgs<T> g;
-    g.q = View<const T>{static_cast<const T*>(v[0].ptr), v[0].batch, v[0].head, v[0].row};
-    g.out = view<T>(v[3]);
-    g.lse = a.lse;
-    g.seg[0] = KeySeg<T>{view<const T>(v[1]), view<const T>(v[2]), a.k_len, a.m, 0};
-    g.seg[1] = g.seg[0];
-    g.nseg = 1;
-    g.B = a.B;
-    g.Hkv = a.Hkv;
-    g.G = a.Hq / a.Hkv;
-    g.n = a.n;
-    g.cfac = static_cast<float>(static_cast<double>(a.tau) * 1.4426950408889634);
-    launch_fwd<T, D>(g, cross_plan(a), ws, stream);
-}
-
-template <typename T, int D>
-void prefix_fwd(const lard_prefix_attn_args& a, const lard_attn_view (&v)[6], void* ws, cudaStream_t stream) {
-    FwdArgs<T> g;
-    g.q = view<const T>(v[0]);
-    g.out = view<T>(v[5]);
-    g.lse = a.lse;
-    g.nseg = 0;
-    if (a.P > 0) g.seg[g.nseg++] = KeySeg<T>{view<const T>(v[1]), view<const T>(v[2]), nullptr, a.P, 0};
-    if (a.S > 0) g.seg[g.nseg++] = KeySeg<T>{view<const T>(v[3]), view<const T>(v[4]), a.s_len, a.S, 1};
-    if (g.nseg == 1) g.seg[1] = g.seg[0];
-    g.B = a.B;
-    g.Hkv = a.Hkv;
-    g.G = a.Hq / a.Hkv;
-    g.n = a.n;
-    g.cfac = static_cast<float>(static_cast<double>(a.tau) * 1.4426950408889634);
-    launch_fwd<T, D>(g, prefix_plan(a), ws, stream);
+lard_status launch_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t stream) {
+    if (f.dtype == LARD_DTYPE_BF16)
+        return f.d == 64 ? run_fwd<bf16, 64>(f, p, ws, stream) : run_fwd<bf16, 128>(f, p, ws, stream);
+    return f.d == 64 ? run_fwd<float, 64>(f, p, ws, stream) : run_fwd<float, 128>(f, p, ws, stream);
 }
 
 // ------------------------------------------------------------------ backward
@@ -300,7 +497,7 @@ size_t bwd_bytes(const lard_cross_attn& a) {
 }
 
 template <typename T, int D>
-void cross_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+lard_status run_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
     using namespace lard::attn;
     BwdArgs<T> g;
     g.q = view<const T>(v[0]);
@@ -319,32 +516,28 @@ void cross_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws,
     g.Hkv = a.Hkv;
     g.G = a.Hq / a.Hkv;
     g.n = a.n;
-    g.cfac = static_cast<float>(static_cast<double>(a.tau) * 1.4426950408889634);
+    g.cfac = log2_factor(a.tau);
     g.tau = a.tau;
     const long long BH = static_cast<long long>(a.B) * a.Hkv, R = static_cast<long long>(g.G) * a.n;
     const long long rtiles = (R + kSimtTile - 1) / kSimtTile;
     attn_delta_kernel<T, D><<<static_cast<unsigned>((BH * R + 7) / 8), 256, 0, stream>>>(g);
-    attn_dkdv_simt_kernel<T, D><<<static_cast<unsigned>(BH * key_tiles(a.m)), kSimtThreads, SimtLayout<D>::BWD_BYTES, stream>>>(g);
+    attn_dkdv_simt_kernel<T, D><<<static_cast<unsigned>(BH * tiles_of(a.m, kSimtTile)), kSimtThreads, SimtLayout<D>::BWD_BYTES, stream>>>(g);
     attn_dq_simt_kernel<T, D><<<static_cast<unsigned>(BH * rtiles), kSimtThreads, SimtLayout<D>::BWD_BYTES, stream>>>(g);
+    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
 }
 
-#define LARD_ATTN_DISPATCH(dtype, d, F, ...)                         \
-    do {                                                             \
-        if ((dtype) == LARD_DTYPE_BF16) {                            \
-            if ((d) == 64) F<bf16, 64>(__VA_ARGS__);                 \
-            else F<bf16, 128>(__VA_ARGS__);                          \
-        } else {                                                     \
-            if ((d) == 64) F<float, 64>(__VA_ARGS__);                \
-            else F<float, 128>(__VA_ARGS__);                         \
-        }                                                            \
-    } while (0)
+lard_status launch_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+    if (a.dtype == LARD_DTYPE_BF16)
+        return a.d == 64 ? run_bwd<bf16, 64>(a, v, ws, stream) : run_bwd<bf16, 128>(a, v, ws, stream);
+    return a.d == 64 ? run_bwd<float, 64>(a, v, ws, stream) : run_bwd<float, 128>(a, v, ws, stream);
+}
 
 }  // namespace
 
 extern "C" {
 
 size_t lard_cross_attn_fwd_workspace_bytes(const lard_cross_attn* a) {
-    return cross_sizes(a) == LARD_OK ? cross_plan(*a).bytes() : 0;
+    return cross_sizes(a) == LARD_OK ? plan_fwd(cross_work(*a)).bytes() : 0;
 }
 
 size_t lard_cross_attn_bwd_workspace_bytes(const lard_cross_attn* a) {
@@ -352,7 +545,7 @@ size_t lard_cross_attn_bwd_workspace_bytes(const lard_cross_attn* a) {
 }
 
 size_t lard_prefix_attn_workspace_bytes(const lard_prefix_attn_args* a) {
-    return prefix_sizes(a) == LARD_OK ? prefix_plan(*a).bytes() : 0;
+    return prefix_sizes(a) == LARD_OK ? plan_fwd(prefix_work(*a)).bytes() : 0;
 }
 
 lard_status lard_cross_attn_fwd(const lard_cross_attn* a, void* workspace, size_t workspace_bytes,
@@ -369,7 +562,9 @@ lard_status lard_cross_attn_fwd(const lard_cross_attn* a, void* workspace, size_
         !bufs.add_view(a->out, a->B, a->Hq, a->n, a->d, e, true, &v[3]))
         return LARD_ERR_INVALID_ARG;
     if (!a->lse || !aligned(a->lse, 4) || (a->k_len && !aligned(a->k_len, 4))) return LARD_ERR_INVALID_ARG;
-    const size_t need = cross_plan(*a).bytes();
+    const Fwd work = cross_work(*a, v);
+    const FwdPlan plan = plan_fwd(work);
+    const size_t need = plan.bytes();
     if (!workspace_ok(workspace, workspace_bytes, need)) return LARD_ERR_INVALID_ARG;
     bufs.add_flat(a->lse, static_cast<size_t>(a->B) * a->Hq * a->n * 4, true);
     bufs.add_flat(a->k_len, static_cast<size_t>(a->B) * 4, false);
@@ -378,8 +573,7 @@ lard_status lard_cross_attn_fwd(const lard_cross_attn* a, void* workspace, size_
     DeviceGuard guard;
     st = bufs.select_device();
     if (st != LARD_OK) return st;
-    LARD_ATTN_DISPATCH(a->dtype, a->d, cross_fwd, *a, v, workspace, stream);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    return launch_fwd(work, plan, workspace, stream);
 }
 
 lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_t workspace_bytes,
@@ -409,8 +603,7 @@ lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_
     DeviceGuard guard;
     st = bufs.select_device();
     if (st != LARD_OK) return st;
-    LARD_ATTN_DISPATCH(a->dtype, a->d, cross_bwd, *a, v, workspace, stream);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    return launch_bwd(*a, v, workspace, stream);
 }
 
 lard_status lard_prefix_attn(const lard_prefix_attn_args* a, void* workspace, size_t workspace_bytes,
@@ -430,7 +623,9 @@ lard_status lard_prefix_attn(const lard_prefix_attn_args* a, void* workspace, si
         return LARD_ERR_INVALID_ARG;
     if (!bufs.add_view(a->out, a->B, a->Hq, a->n, a->d, e, true, &v[5])) return LARD_ERR_INVALID_ARG;
     if (!a->lse || !aligned(a->lse, 4) || (a->S > 0 && a->s_len && !aligned(a->s_len, 4))) return LARD_ERR_INVALID_ARG;
-    const size_t need = prefix_plan(*a).bytes();
+    const Fwd work = prefix_work(*a, v);
+    const FwdPlan plan = plan_fwd(work);
+    const size_t need = plan.bytes();
     if (!workspace_ok(workspace, workspace_bytes, need)) return LARD_ERR_INVALID_ARG;
     bufs.add_flat(a->lse, static_cast<size_t>(a->B) * a->Hq * a->n * 4, true);
     if (a->S > 0) bufs.add_flat(a->s_len, static_cast<size_t>(a->B) * 4, false);
@@ -439,8 +634,7 @@ lard_status lard_prefix_attn(const lard_prefix_attn_args* a, void* workspace, si
     DeviceGuard guard;
     st = bufs.select_device();
     if (st != LARD_OK) return st;
-    LARD_ATTN_DISPATCH(a->dtype, a->d, prefix_fwd, *a, v, workspace, stream);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    return launch_fwd(work, plan, workspace, stream);
 }
 
 lard_status lard_attn_device_status(cudaStream_t stream, unsigned int* fault_bits) {
