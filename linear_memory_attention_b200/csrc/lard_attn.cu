@@ -13,6 +13,7 @@
 #include "lard_attn.h"
 #include "lard_host.h"
 #include "lard_kernel_common.cuh"
+#include "attn/attn_bwd_tc.cuh"
 #include "attn/attn_common.cuh"
 #include "attn/attn_fwd_tc.cuh"
 #include "attn/attn_simt.cuh"
@@ -54,26 +55,27 @@ lard_status setup_device(int dev) {
     if (st == LARD_OK) {
         using namespace lard::attn;
         bool ok = true, fits = true;
-        auto fwd_tc = [&](auto kernel, int smem) {
+        auto tc = [&](auto kernel, int smem, int threads, int regs) {
             ok = ok && set_smem(kernel, smem) == cudaSuccess;
-            fits = fits && split_fits(kernel, kFwdTcThreads, kFwdTcRegsSplitTotal);
+            fits = fits && split_fits(kernel, threads, regs);
         };
-        fwd_tc(attn_fwd_tc_kernel<64, 0>, FwdTcLayout<64>::SMEM_BYTES);
-        fwd_tc(attn_fwd_tc_kernel<64, 1>, FwdTcLayout<64>::SMEM_BYTES);
-        fwd_tc(attn_fwd_tc_kernel<128, 0>, FwdTcLayout<128>::SMEM_BYTES);
-        fwd_tc(attn_fwd_tc_kernel<128, 1>, FwdTcLayout<128>::SMEM_BYTES);
-        auto simt = [&](auto t, auto d) {
-            using T = decltype(t);
+        auto tc_d = [&](auto d) {
             constexpr int D = decltype(d)::value;
-            if constexpr (std::is_same<T, float>::value)
-                ok = ok && set_smem(attn_fwd_simt_kernel<T, D>, SimtLayout<D>::FWD_BYTES) == cudaSuccess;
-            ok = ok && set_smem(attn_dkdv_simt_kernel<T, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess &&
-                 set_smem(attn_dq_simt_kernel<T, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess;
+            tc(attn_fwd_tc_kernel<D, 0>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
+            tc(attn_fwd_tc_kernel<D, 1>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
+            tc(attn_dq_tc_kernel<D>, DqLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
+            tc(attn_dkdv_tc_kernel<D>, DkvLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
         };
-        simt(float(), std::integral_constant<int, 64>());
-        simt(float(), std::integral_constant<int, 128>());
-        simt(bf16(), std::integral_constant<int, 64>());
-        simt(bf16(), std::integral_constant<int, 128>());
+        tc_d(std::integral_constant<int, 64>());
+        tc_d(std::integral_constant<int, 128>());
+        auto simt = [&](auto d) {
+            constexpr int D = decltype(d)::value;
+            ok = ok && set_smem(attn_fwd_simt_kernel<float, D>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
+                 set_smem(attn_dkdv_simt_kernel<float, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess &&
+                 set_smem(attn_dq_simt_kernel<float, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess;
+        };
+        simt(std::integral_constant<int, 64>());
+        simt(std::integral_constant<int, 128>());
         if (!ok) st = LARD_ERR_CUDA;
         else if (!fits) st = LARD_ERR_UNSUPPORTED;  // a build whose register count cannot host the split
     }
@@ -313,17 +315,18 @@ FwdPlan plan_fwd(const Fwd& f) {
     return p;
 }
 
-// 4-D tensor map of a K or V tensor with 64 x 128 boxes, 128-byte swizzle; rows
-// past the end read as zeros.  A dimension of one element, or of one block for all
-// (stride 0), has one entry.
-bool make_kv_map(CUtensorMap* m, const lard_attn_view& v, long long B, long long H, long long rows, int d) {
+// 4-D tensor map of a bf16 tensor with boxes of 64 columns x box_rows rows,
+// 128-byte swizzle; rows past the end read as zeros.  A dimension of one
+// element, or of one block for all (stride 0), has one entry.
+bool make_map(CUtensorMap* m, const lard_attn_view& v, long long B, long long H, long long rows, int d,
+              unsigned box_rows = 128) {
     const cuuint64_t line = static_cast<cuuint64_t>(d) * 2;
     cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(rows),
                           static_cast<cuuint64_t>(v.head ? H : 1), static_cast<cuuint64_t>(v.batch ? B : 1)};
     cuuint64_t strides[3] = {v.row ? static_cast<cuuint64_t>(v.row) * 2 : line,
                              v.head ? static_cast<cuuint64_t>(v.head) * 2 : line,
                              v.batch ? static_cast<cuuint64_t>(v.batch) * 2 : line};
-    cuuint32_t box[4] = {64, 128, 1, 1};
+    cuuint32_t box[4] = {64, box_rows, 1, 1};
     cuuint32_t estr[4] = {1, 1, 1, 1};
     return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, v.ptr, dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -381,8 +384,8 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
         for (int k = 0; k < p.npass; ++k) {
             const Fwd::Seg& x = f.seg[k];
             TcSeg& s = a.seg[0];
-            if (!make_kv_map(&s.k, x.k, x.shared ? 1 : f.B, f.Hkv, x.rows, D) ||
-                !make_kv_map(&s.v, x.v, x.shared ? 1 : f.B, f.Hkv, x.rows, D))
+            if (!make_map(&s.k, x.k, x.shared ? 1 : f.B, f.Hkv, x.rows, D) ||
+                !make_map(&s.v, x.v, x.shared ? 1 : f.B, f.Hkv, x.rows, D))
                 return LARD_ERR_INVALID_ARG;
             s.len = x.len;
             s.cap = x.rows;
@@ -496,9 +499,51 @@ size_t bwd_bytes(const lard_cross_attn& a) {
     return (static_cast<size_t>(a.B) * a.Hq * a.n * 4 + 15) / 16 * 16;  // delta
 }
 
-template <typename T, int D>
-lard_status run_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+template <int D>
+lard_status run_bwd_tc(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
     using namespace lard::attn;
+    TcBwdArgs g;
+    if (!make_map(&g.k, v[1], a.B, a.Hkv, a.m, D) || !make_map(&g.v, v[2], a.B, a.Hkv, a.m, D) ||
+        !make_map(&g.q64, v[0], a.B, a.Hq, a.n, D, kUnit) || !make_map(&g.do64, v[4], a.B, a.Hq, a.n, D, kUnit))
+        return LARD_ERR_INVALID_ARG;
+    g.q = view<const bf16>(v[0]);
+    g.out = view<const bf16>(v[3]);
+    g.dout = view<const bf16>(v[4]);
+    g.dq = view<bf16>(v[5]);
+    g.dk = view<bf16>(v[6]);
+    g.dv = view<bf16>(v[7]);
+    g.lse = a.lse;
+    g.delta = static_cast<float*>(ws);
+    g.len = a.k_len;
+    g.m = a.m;
+    g.B = a.B;
+    g.Hkv = a.Hkv;
+    g.G = a.Hq / a.Hkv;
+    g.n = a.n;
+    g.khead = v[1].head != 0;
+    g.kbatch = v[1].batch != 0;
+    g.vhead = v[2].head != 0;
+    g.vbatch = v[2].batch != 0;
+    g.qhead = v[0].head != 0;
+    g.qbatch = v[0].batch != 0;
+    g.dohead = v[4].head != 0;
+    g.dobatch = v[4].batch != 0;
+    g.cfac = log2_factor(a.tau);
+    g.tau = a.tau;
+    g.wait_ns = kWaitLimitNs;
+    g.drain_ns = kDrainLimitNs;
+    const long long BH = static_cast<long long>(a.B) * a.Hkv, R = static_cast<long long>(g.G) * a.n;
+    attn_dq_tc_kernel<D>
+        <<<static_cast<unsigned>(BH * tiles_of(R, 128)), kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream>>>(g);
+    attn_dkdv_tc_kernel<D>
+        <<<static_cast<unsigned>(BH * tiles_of(a.m, 128)), kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream>>>(g);
+    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+}
+
+template <int D>
+lard_status run_bwd_simt(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+    using namespace lard::attn;
+    using T = float;
     BwdArgs<T> g;
     g.q = view<const T>(v[0]);
     g.k = view<const T>(v[1]);
@@ -528,8 +573,8 @@ lard_status run_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void
 
 lard_status launch_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
     if (a.dtype == LARD_DTYPE_BF16)
-        return a.d == 64 ? run_bwd<bf16, 64>(a, v, ws, stream) : run_bwd<bf16, 128>(a, v, ws, stream);
-    return a.d == 64 ? run_bwd<float, 64>(a, v, ws, stream) : run_bwd<float, 128>(a, v, ws, stream);
+        return a.d == 64 ? run_bwd_tc<64>(a, v, ws, stream) : run_bwd_tc<128>(a, v, ws, stream);
+    return a.d == 64 ? run_bwd_simt<64>(a, v, ws, stream) : run_bwd_simt<128>(a, v, ws, stream);
 }
 
 }  // namespace
