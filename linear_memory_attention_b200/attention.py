@@ -40,6 +40,7 @@ EXPORTS = ("lard_cross_attn_fwd_workspace_bytes", "lard_cross_attn_bwd_workspace
 _CROSS = struct.Struct("7if" + "4q" * 3 + "q" + "4q" + "q" + "4q" * 4)
 _PREFIX = struct.Struct("8if4x" + "4q" * 5 + "q" + "4q" + "q")
 _NO_VIEW = (0, 0, 0, 0)
+_NO_GRADS = _NO_VIEW * 4
 
 
 def _load() -> ctypes.CDLL:
@@ -63,6 +64,17 @@ def _load() -> ctypes.CDLL:
 _lib = _load()
 
 
+def _current_stream(device: int) -> int:
+    if device < 0:
+        raise ValueError("tensors must be on a GPU")
+    return _raw_stream(device)
+
+
+# torch.cuda.current_stream builds a Stream object, which costs more than the C call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 def _dtype(t):
     if t.dtype == torch.bfloat16:
         return LARD_DTYPE_BF16
@@ -71,27 +83,38 @@ def _dtype(t):
     raise ValueError(f"unsupported dtype {t.dtype}")
 
 
-def _view(t, shape, q, name):
-    """The fields of a lard_attn_view of t, which must have this shape and q's dtype and device."""
+def _refuse(t, shape, dtype, q, name):
+    """The reason why t is not such a tensor."""
     if t.shape != shape:
         raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.dtype != q.dtype:
-        raise ValueError(f"{name}: expected {q.dtype}, got {t.dtype}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name}: expected {dtype}, got {t.dtype}")
     if t.device != q.device:
         raise ValueError(f"{name}: on {t.device}, q on {q.device}")
-    st = t.stride()
-    if st[-1] != 1:
-        raise ValueError(f"{name}: the last dimension must be contiguous")
-    return (t.data_ptr(), *st[:-1]) if len(st) == 4 else (t.data_ptr(), 0, *st[:-1])
+    raise ValueError(f"{name}: must be contiguous (its last dimension, where views are taken)")
+
+
+def _view(t, shape, q, name):
+    """The fields of a lard_attn_view of t [B, H, rows, d], which must have this shape and q's
+    dtype and device."""
+    batch, head, row, one = t.stride()
+    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device() or one != 1:
+        _refuse(t, shape, q.dtype, q, name)
+    return t.data_ptr(), batch, head, row
+
+
+def _shared(t, shape, q, name):
+    """The fields of a lard_attn_view of t [H, rows, d], one block for all sequences."""
+    head, row, one = t.stride()
+    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device() or one != 1:
+        _refuse(t, shape, q.dtype, q, name)
+    return t.data_ptr(), 0, head, row
 
 
 def _flat(t, shape, dtype, q, name):
     """The address of a contiguous tensor of this shape and dtype on q's device."""
-    if t.shape != shape or t.dtype != dtype or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)}, "
-                         f"got {t.dtype} {tuple(t.shape)}")
-    if t.device != q.device:
-        raise ValueError(f"{name}: on {t.device}, q on {q.device}")
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != q.get_device() or not t.is_contiguous():
+        _refuse(t, shape, dtype, q, name)
     return t.data_ptr()
 
 
@@ -110,8 +133,9 @@ def _workspace(ws, need, q):
 
 
 def _handle(stream, q):
+    """The CUDA stream to enqueue on: the given one, or the current one of q's GPU."""
     if stream is None:
-        return torch.cuda.current_stream(q.device).cuda_stream
+        return _current_stream(q.get_device())
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
 
@@ -126,7 +150,8 @@ def _cross_sizes(q, k):
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must be [B, H, rows, d]")
     B, Hq, n, d = q.shape
-    return _dtype(q), B, Hq, k.shape[1], n, k.shape[2], d
+    _, Hkv, m, _ = k.shape
+    return _dtype(q), B, Hq, Hkv, n, m, d
 
 
 def _cross_bytes(fn, sizes):
@@ -146,8 +171,8 @@ def lard_cross_attn_bwd_workspace_bytes(q, k) -> int:
 def _cross_args(q, k, v, tau, k_len, out, lse, grads=None):
     sizes = _cross_sizes(q, k)
     _, B, Hq, Hkv, n, m, d = sizes
-    qs, ks = q.shape, (B, Hkv, m, d)
-    grad_views = _NO_VIEW * 4
+    qs, ks = (B, Hq, n, d), (B, Hkv, m, d)
+    grad_views = _NO_GRADS
     if grads is not None:
         dout, dq, dk, dv = grads
         grad_views = (*_view(dout, qs, q, "dout"), *_view(dq, qs, q, "dq"), *_view(dk, ks, q, "dk"),
@@ -192,9 +217,11 @@ def lard_prefix_attn_workspace_bytes(q, kp, ks) -> int:
 def _prefix_args(q, kp, vp, ks, vs, s_len, tau, out, lse):
     if (kp is None) != (vp is None) or (ks is None) != (vs is None):
         raise ValueError("keys and values are given together")
+    if (vp is not None and vp.dim() != 3) or (vs is not None and vs.dim() != 4):
+        raise ValueError("vp must be [H, rows, d], vs [B, H, rows, d]")
     sizes = _prefix_sizes(q, kp, ks)
     _, B, Hq, Hkv, n, P, S, d = sizes
-    views = _NO_VIEW * 2 if kp is None else (*_view(kp, (Hkv, P, d), q, "kp"), *_view(vp, (Hkv, P, d), q, "vp"))
+    views = _NO_VIEW * 2 if kp is None else (*_shared(kp, (Hkv, P, d), q, "kp"), *_shared(vp, (Hkv, P, d), q, "vp"))
     own = _NO_VIEW * 2 if ks is None else (*_view(ks, (B, Hkv, S, d), q, "ks"), *_view(vs, (B, Hkv, S, d), q, "vs"))
     return _PREFIX.pack(*sizes, tau, *_view(q, q.shape, q, "q"), *views, *own,
                         0 if s_len is None else _flat(s_len, (B,), torch.int32, q, "s_len"),
@@ -218,7 +245,13 @@ def _on(stream):
 
 
 def _bytes(need, q):
-    return torch.empty((need,), device=q.device, dtype=torch.uint8) if need else None
+    return torch.empty_strided((need,), (1,), device=q.device, dtype=torch.uint8) if need else None
+
+
+def _outputs(q):
+    """out in q's layout, lse [B, Hq, n]."""
+    B, Hq, n, _ = q.shape
+    return torch.empty_like(q), torch.empty_strided((B, Hq, n), (Hq * n, n, 1), device=q.device, dtype=torch.float32)
 
 
 def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
@@ -229,7 +262,9 @@ def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
     if stream is not None:
         with _on(stream):
             return cross_attention(q, k, v, tau, k_len, dout)
-    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, rows, d]")
+    out, lse = _outputs(q)
     grads = None if dout is None else (dout, torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
     args = _cross_args(q, k, v, tau, k_len, out, lse, grads)
     need = _lib.lard_cross_attn_fwd_workspace_bytes(args)
@@ -247,7 +282,9 @@ def prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream=None):
     if stream is not None:
         with _on(stream):
             return prefix_attention(q, kp, vp, ks, vs, s_len, tau)
-    out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device=q.device, dtype=torch.float32)
+    if q.dim() != 4:
+        raise ValueError("q must be [B, H, rows, d]")
+    out, lse = _outputs(q)
     args = _prefix_args(q, kp, vp, ks, vs, s_len, tau, out, lse)
     need = _lib.lard_prefix_attn_workspace_bytes(args)
     _call(_lib.lard_prefix_attn, "lard_prefix_attn", args, _bytes(need, q), need, q, None)

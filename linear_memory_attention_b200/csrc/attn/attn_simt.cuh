@@ -224,6 +224,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     for (int s = 0; s < g.splits; ++s) {
         const float w = exp2f((g.part_lse[s * rows + row] - base) * kLog2e);
         total += w;
+        if (w == 0.f) continue;  // a split that saw nothing need not have written its O
         const float* src = g.part_o + (s * rows + row) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);

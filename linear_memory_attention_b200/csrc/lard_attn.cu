@@ -15,6 +15,7 @@
 #include "lard_kernel_common.cuh"
 #include "attn/attn_bwd_tc.cuh"
 #include "attn/attn_common.cuh"
+#include "attn/attn_few.cuh"
 #include "attn/attn_fwd_tc.cuh"
 #include "attn/attn_simt.cuh"
 
@@ -63,6 +64,7 @@ lard_status setup_device(int dev) {
             constexpr int D = decltype(d)::value;
             tc(attn_fwd_tc_kernel<D, 0>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
             tc(attn_fwd_tc_kernel<D, 1>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
+            ok = ok && set_smem(attn_few_kernel<D>, FewLayout<D>::SMEM_BYTES) == cudaSuccess;
             tc(attn_dq_tc_kernel<D>, DqLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
             tc(attn_dkdv_tc_kernel<D>, DkvLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
         };
@@ -217,8 +219,12 @@ long long tiles_of(long long rows, int tile) { return (rows + tile - 1) / tile; 
 // One pass over the keys of a call: PB problems per key head of R rows each
 // over at most `tiles` key tiles, the key axis dealt to `splits` blocks.
 struct Pass {
-    long long blocks = 0;
-    int splits = 0, by_keys = 0;
+    enum Kind { kSimt, kTcRows, kTcKeys, kFew } kind = kSimt;
+    long long blocks = 0;  // of one split
+    int splits = 0;
+    int nseg = 1, seg = 0;  // segments [seg, seg + nseg)
+    int shared = 0;         // one problem per key head over all sequences' rows
+    int cluster = 1;  // kFew: blocks of a cluster, which share a problem's keys
 };
 
 // A forward call: one pass, or two (prefix attention: the shared keys, then
@@ -259,16 +265,17 @@ Pass plan_simt(long long problems, long long R, long long tiles) {
 // brings the tiles of all running blocks.
 Pass plan_tc(long long problems, long long R, int d, long long tiles, long long rows) {
     Pass p;
-    p.by_keys = R <= 128;
-    const long long rtiles = tiles_of(R, p.by_keys ? 128 : 256);
+    const bool by_keys = R <= 128;
+    p.kind = by_keys ? Pass::kTcKeys : Pass::kTcRows;
+    const long long rtiles = tiles_of(R, by_keys ? 128 : 256);
     p.blocks = problems * rtiles;
     double best = 0.0;
-    const long long most = std::max(1LL, std::min(64LL, p.by_keys ? tiles / 2 : tiles));
+    const long long most = std::max(1LL, std::min(64LL, by_keys ? tiles / 2 : tiles));
     for (long long s = 1; s <= most; ++s) {
         const long long waves = tiles_of(p.blocks * s, kSms), running = std::min<long long>(kSms, p.blocks * s);
-        const double steps = static_cast<double>(tiles_of(tiles_of(tiles, s), p.by_keys ? 2 : 1));
+        const double steps = static_cast<double>(tiles_of(tiles_of(tiles, s), by_keys ? 2 : 1));
         double step = 2200.0;
-        if (rtiles == 1) step = std::max(step, (p.by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
+        if (rtiles == 1) step = std::max(step, (by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
         double cost = waves * (steps * step + 6000.0);
         if (s > 1) cost += 8000.0 + 8.0 * s * rows * d / 3400.0;
         if (s == 1 || cost < best) {
@@ -276,6 +283,39 @@ Pass plan_tc(long long problems, long long R, int d, long long tiles, long long 
             p.splits = static_cast<int>(s);
         }
     }
+    return p;
+}
+
+// Pass of at most 16 rows a problem.  A problem's keys are dealt to a cluster of
+// up to eight blocks of four warps, which join their rows without a second
+// kernel.  The size is the one with the least time, in us, by a model: three
+// blocks an SM run at a time; a warp takes a group of 16 keys in 1 us, or in the
+// time that HBM needs for one group of every running warp; a round of blocks
+// has 3 us of its own.  (128 problems of 8000 keys at d = 128: 3 blocks each
+// fill one round, 84 us; 8 fill 2.3, 97 us.)  Where eight blocks leave
+// SMs idle (few problems of many keys), several clusters share a problem and the join
+// kernel joins them.
+Pass plan_few(long long problems, long long groups, int d) {
+    Pass p;
+    p.kind = Pass::kFew;
+    const long long slots = 3 * kSms;
+    double best = 0.0;
+    for (int c = 1; c <= 8; ++c) {
+        const long long blocks = problems * c, full = blocks / slots, rest = blocks % slots;
+        const double rounds = static_cast<double>(tiles_of(groups, lard::attn::kFewWarps * c));
+        auto time = [&](long long running) {
+            return rounds * std::max(1.0, running * lard::attn::kFewWarps * 64.0 * d / 6.5e6) + 3.0;
+        };
+        const double cost = full * time(slots) + (rest ? time(rest) : 0.0);
+        if (c == 1 || cost < best) {
+            best = cost;
+            p.cluster = c;
+        }
+    }
+    p.blocks = problems * p.cluster;
+    p.splits = 1;
+    if (p.blocks < 2 * kSms)
+        p.splits = static_cast<int>(std::max(1LL, std::min(slots / p.blocks, groups / (16 * p.cluster * lard::attn::kFewWarps))));
     return p;
 }
 
@@ -307,10 +347,29 @@ FwdPlan plan_fwd(const Fwd& f) {
         p.pass[p.npass++] = plan_simt(own, f.group_rows(), tiles);
         return p;
     }
-    for (int s = 0; s < f.nseg; ++s) {
-        const bool shared = f.seg[s].shared;
-        p.pass[p.npass++] = plan_tc(shared ? f.Hkv : own, f.group_rows() * (shared ? f.B : 1), f.d,
-                                    tiles_of(f.seg[s].rows, 128), p.rows);
+    auto tc_or_few = [&](int seg, int nseg, bool shared) {
+        const long long problems = shared ? f.Hkv : own, R = f.group_rows() * (shared ? f.B : 1);
+        long long tiles = 0, groups = 0;
+        for (int s = seg; s < seg + nseg; ++s) {
+            tiles += tiles_of(f.seg[s].rows, 128);
+            groups += tiles_of(f.seg[s].rows, 16);
+        }
+        Pass x = R <= lard::attn::kFewRows ? plan_few(problems, groups, f.d) : plan_tc(problems, R, f.d, tiles, p.rows);
+        x.seg = seg;
+        x.nseg = nseg;
+        x.shared = shared;
+        p.pass[p.npass++] = x;
+    };
+    // A shared prefix is read once for all sequences, in a pass of its own, unless
+    // there is one sequence, or so little to read again (from L2) that a pass and a join
+    // cost more: they take about 7 us, in which L2 brings some 16 MB to blocks
+    // that wait for them.
+    const double again = static_cast<double>(f.B) * f.Hkv * f.seg[0].rows * f.d * 4.0;
+    if (f.nseg == 2 && f.B > 1 && !(f.group_rows() <= lard::attn::kFewRows && again <= 16.0e6)) {
+        tc_or_few(0, 1, true);
+        tc_or_few(1, 1, false);
+    } else {
+        tc_or_few(0, f.nseg, f.nseg == 1 && f.B > 1 && f.seg[0].shared);
     }
     return p;
 }
@@ -354,6 +413,89 @@ FwdArgs<T> fwd_args(const Fwd& f) {
     return g;
 }
 
+// What the passes' arguments have in common.
+template <typename A>
+void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<bf16>& g) {
+    a.q = g.q;
+    a.out = g.out;
+    a.lse = g.lse;
+    a.nseg = x.nseg;
+    a.PB = x.shared ? 1 : f.B;
+    a.Hkv = g.Hkv;
+    a.G = g.G;
+    a.n = g.n;
+    a.R = static_cast<int>(f.group_rows() * (x.shared ? f.B : 1));
+    a.split0 = split0;
+    a.join = p.join();
+    a.rows = p.rows;
+    a.part_o = g.part_o;
+    a.part_lse = g.part_lse;
+    a.cfac = g.cfac;
+}
+
+// The key segments of a pass for TMA loads of box_rows rows.
+bool make_segs(lard::attn::TcSeg (&seg)[2], const Fwd& f, const Pass& x, unsigned box_rows) {
+    for (int k = 0; k < x.nseg; ++k) {
+        const Fwd::Seg& y = f.seg[x.seg + k];
+        lard::attn::TcSeg& s = seg[k];
+        if (!make_map(&s.k, y.k, y.shared ? 1 : f.B, f.Hkv, y.rows, f.d, box_rows) ||
+            !make_map(&s.v, y.v, y.shared ? 1 : f.B, f.Hkv, y.rows, f.d, box_rows))
+            return false;
+        s.len = y.len;
+        s.cap = y.rows;
+        s.causal = y.causal;
+        s.khead = y.k.head != 0;
+        s.kbatch = y.k.batch != 0;
+        s.vhead = y.v.head != 0;
+        s.vbatch = y.v.batch != 0;
+    }
+    if (x.nseg == 1) seg[1] = seg[0];
+    return true;
+}
+
+template <int D>
+lard_status run_few(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<bf16>& g,
+                    cudaStream_t stream) {
+    using namespace lard::attn;
+    FewArgs a;
+    pass_args(a, f, p, x, split0, g);
+    if (!make_segs(a.seg, f, x, 16)) return LARD_ERR_INVALID_ARG;
+    a.cluster = x.cluster;
+    a.splits = x.splits;
+    a.wait_ns = kWaitLimitNs;
+    a.drain_ns = kDrainLimitNs;
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(static_cast<unsigned>(x.blocks * x.splits));
+    c.blockDim = dim3(32 * kFewWarps);
+    c.dynamicSmemBytes = FewLayout<D>::SMEM_BYTES;
+    c.stream = stream;
+    cudaLaunchAttribute at;
+    at.id = cudaLaunchAttributeClusterDimension;
+    at.val.clusterDim.x = static_cast<unsigned>(x.cluster);
+    at.val.clusterDim.y = at.val.clusterDim.z = 1;
+    c.attrs = &at;
+    c.numAttrs = 1;
+    return cudaLaunchKernelEx(&c, attn_few_kernel<D>, a) == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+}
+
+template <int D>
+lard_status run_tc(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<bf16>& g,
+                   cudaStream_t stream) {
+    using namespace lard::attn;
+    TcFwdArgs a;
+    pass_args(a, f, p, x, split0, g);
+    if (!make_segs(a.seg, f, x, 128)) return LARD_ERR_INVALID_ARG;
+    a.splits = x.splits;
+    a.wait_ns = kWaitLimitNs;
+    a.drain_ns = kDrainLimitNs;
+    const unsigned grid = static_cast<unsigned>(x.blocks * x.splits);
+    if (x.kind == Pass::kTcKeys)
+        attn_fwd_tc_kernel<D, 1><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
+    else
+        attn_fwd_tc_kernel<D, 0><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
+    return LARD_OK;
+}
+
 template <typename T, int D>
 lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t stream) {
     using namespace lard::attn;
@@ -365,45 +507,12 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
         attn_fwd_simt_kernel<T, D>
             <<<static_cast<unsigned>(p.pass[0].blocks * p.pass[0].splits), kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(g);
     } else {
-        TcFwdArgs a;
-        a.q = g.q;
-        a.out = g.out;
-        a.lse = g.lse;
-        a.nseg = 1;
-        a.Hkv = g.Hkv;
-        a.G = g.G;
-        a.n = g.n;
-        a.join = p.join();
-        a.rows = p.rows;
-        a.part_o = g.part_o;
-        a.part_lse = g.part_lse;
-        a.cfac = g.cfac;
-        a.wait_ns = kWaitLimitNs;
-        a.drain_ns = kDrainLimitNs;
-        a.split0 = 0;
+        int split0 = 0;
         for (int k = 0; k < p.npass; ++k) {
-            const Fwd::Seg& x = f.seg[k];
-            TcSeg& s = a.seg[0];
-            if (!make_map(&s.k, x.k, x.shared ? 1 : f.B, f.Hkv, x.rows, D) ||
-                !make_map(&s.v, x.v, x.shared ? 1 : f.B, f.Hkv, x.rows, D))
-                return LARD_ERR_INVALID_ARG;
-            s.len = x.len;
-            s.cap = x.rows;
-            s.causal = x.causal;
-            s.khead = x.k.head != 0;
-            s.kbatch = x.k.batch != 0;
-            s.vhead = x.v.head != 0;
-            s.vbatch = x.v.batch != 0;
-            a.seg[1] = s;
-            a.PB = x.shared ? 1 : f.B;
-            a.R = static_cast<int>(f.group_rows() * (x.shared ? f.B : 1));
-            a.splits = p.pass[k].splits;
-            const unsigned grid = static_cast<unsigned>(p.pass[k].blocks * p.pass[k].splits);
-            if (p.pass[k].by_keys)
-                attn_fwd_tc_kernel<D, 1><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
-            else
-                attn_fwd_tc_kernel<D, 0><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
-            a.split0 += p.pass[k].splits;
+            const lard_status st = p.pass[k].kind == Pass::kFew ? run_few<D>(f, p, p.pass[k], split0, g, stream)
+                                                                : run_tc<D>(f, p, p.pass[k], split0, g, stream);
+            if (st != LARD_OK) return st;
+            split0 += p.pass[k].splits;
         }
     }
     if (p.join())

@@ -85,6 +85,7 @@ def test_valid_arguments_reach_the_device_check(att):
     are those of the argument checks; with one, the made-up addresses are refused there."""
     end = 1 if torch.cuda.is_available() else 3
     assert cross_call(att) == end and cross_call(att, "bwd") == end and prefix_call(att) == end
+    assert prefix_call(att, P=100000) == end
     assert cross_call(att, k_batch=0, v_head=0) == end                 # inputs may be shared
     assert cross_call(att, B=1, q_batch=7, out_batch=3) == end         # the stride of one element is not used
     assert prefix_call(att, P=0, kp_ptr=None, vp_ptr=None) == end
@@ -142,7 +143,7 @@ def prefix_call(att, ws=40 * STEP, **kw):
 @pytest.mark.parametrize("kw", [
     dict(P=-1), dict(S=-1), dict(P=0, S=0), dict(n=0), dict(Hq=5), dict(tau=-1.0), dict(kp_ptr=None), dict(vs_ptr=None),
     dict(kp_row=65), dict(vp_head=-64), dict(ks_batch=4), dict(s_len=20 * STEP + 2), dict(out_ptr=STEP),
-    dict(lse=None), dict(ws=40 * STEP + 8), dict(ws=None), dict(ws=6 * STEP),
+    dict(lse=None), dict(P=100000, ws=40 * STEP + 8), dict(P=100000, ws=None), dict(P=100000, ws=6 * STEP),
 ])
 def test_prefix_refuses(att, kw):
     assert prefix_call(att, **kw) == 1
@@ -188,9 +189,9 @@ def test_workspace_grows_with_what_is_split(att):
     rows need none."""
     bf = torch.bfloat16
     few, many = torch.empty((1, 8, 1, 128), dtype=bf), torch.empty((8, 32, 1, 128), dtype=bf).expand(8, 32, 4096, 128)
-    keys = torch.empty((1, 8, 1, 128), dtype=bf).expand(1, 8, 8000, 128)
+    keys = torch.empty((1, 8, 1, 128), dtype=bf).expand(1, 8, 100000, 128)
     assert att.lard_cross_attn_fwd_workspace_bytes(few, keys) >= 8 * 129 * 4
-    assert att.lard_cross_attn_fwd_workspace_bytes(many, keys.expand(8, 8, 8000, 128)) == 0
+    assert att.lard_cross_attn_fwd_workspace_bytes(many, keys.expand(8, 8, 100000, 128)) == 0
 
 
 def test_missing_library_is_an_import_error(tmp_path):
