@@ -38,9 +38,10 @@ struct KeySeg {
     }
 };
 
-// Forward work: for each (sequence b, key head) the G * n query rows that read
-// that key head, row r = g * n + i being query head hk * G + g, row i.
-// The keys are those of one or two segments, one after the other.
+// Forward work over one or two key segments, one after the other: PB problems
+// per key head, of R query rows each; row r of problem pb is sequence
+// b = pb + r / (G n), query head hk G + r % (G n) / n, row r % n.
+// (Keys of their own: PB = B, R = G n.  Shared keys: PB = 1, R = B G n.)
 template <typename T>
 struct FwdArgs {
     View<const T> q;
@@ -48,13 +49,14 @@ struct FwdArgs {
     float* lse;  // [B, Hq, n]
     KeySeg<T> seg[2];
     int nseg;
-    int B, Hkv, G, n;
+    int PB, Hkv, G, n, R;
     float cfac;  // tau * log2(e): logit -> log2 domain
-    // With splits > 1 the key tiles of a (b, head) are dealt to `splits`
-    // blocks; each leaves its rows' normalised O and LSE here, for the join.
-    int splits;
-    float* part_o;    // [splits][B * Hkv * G * n][D]
-    float* part_lse;  // [splits][B * Hkv * G * n]
+    // With join, the key tiles of a problem are dealt to `splits` blocks, each of
+    // which leaves its rows' normalised O and LSE as partials split0 + split.
+    int splits, split0, join;
+    long long rows;   // B Hkv G n
+    float* part_o;    // [partials][rows][D]
+    float* part_lse;  // [partials][rows]
 };
 
 __device__ __forceinline__ float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }

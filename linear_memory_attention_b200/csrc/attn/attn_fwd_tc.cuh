@@ -46,9 +46,7 @@ struct TcSeg {
     }
 };
 
-// A launch: PB problems per key head, of R rows each; row r of problem pb is
-// sequence b = pb + r / (G n), query head hk G + r % (G n) / n, row r % n.
-// (Keys of their own: PB = B, R = G n.  Shared keys: PB = 1, R = B G n.)
+// A launch; its fields are those of FwdArgs.
 struct TcFwdArgs {
     TcSeg seg[2];
     View<const __nv_bfloat16> q;

@@ -17,11 +17,11 @@
 #include "attn/attn_common.cuh"
 #include "attn/attn_few.cuh"
 #include "attn/attn_fwd_tc.cuh"
+#include "attn/attn_join.cuh"
 #include "attn/attn_simt.cuh"
 
 namespace {
 
-using lard::attn::BwdArgs;
 using lard::attn::FwdArgs;
 using lard::attn::KeySeg;
 using lard::attn::View;
@@ -72,9 +72,10 @@ lard_status setup_device(int dev) {
         tc_d(std::integral_constant<int, 128>());
         auto simt = [&](auto d) {
             constexpr int D = decltype(d)::value;
-            ok = ok && set_smem(attn_fwd_simt_kernel<float, D>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
-                 set_smem(attn_dkdv_simt_kernel<float, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess &&
-                 set_smem(attn_dq_simt_kernel<float, D>, SimtLayout<D>::BWD_BYTES) == cudaSuccess;
+            ok = ok && set_smem(attn_fwd_simt_kernel<D, 2>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
+                 set_smem(attn_fwd_simt_kernel<D, 8>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
+                 set_smem(attn_dkdv_simt_kernel<D>, SimtLayout<D>::DKDV_BYTES) == cudaSuccess &&
+                 set_smem(attn_dq_simt_kernel<D>, SimtLayout<D>::DQ_BYTES) == cudaSuccess;
         };
         simt(std::integral_constant<int, 64>());
         simt(std::integral_constant<int, 128>());
@@ -219,7 +220,7 @@ long long tiles_of(long long rows, int tile) { return (rows + tile - 1) / tile; 
 // One pass over the keys of a call: PB problems per key head of R rows each
 // over at most `tiles` key tiles, the key axis dealt to `splits` blocks.
 struct Pass {
-    enum Kind { kSimt, kTcRows, kTcKeys, kFew } kind = kSimt;
+    enum Kind { kSimt, kSimtFew, kTcRows, kTcKeys, kFew } kind = kSimt;
     long long blocks = 0;  // of one split
     int splits = 0;
     int nseg = 1, seg = 0;  // segments [seg, seg + nseg)
@@ -246,13 +247,22 @@ struct FwdPlan {
     }
 };
 
-// CUDA-core pass: fewer blocks than SMs have the key tiles of each dealt to
-// several blocks, two an SM in all.
-Pass plan_simt(long long problems, long long R, long long tiles) {
+// Blocks that run at once: one an SM at d = 128, two at d = 64 (shared memory).
+int simt_slots(int d) { return d == 64 ? 2 * kSms : kSms; }
+
+// How many blocks share a long axis of `steps` tiles when there are `blocks`
+// without: as many as fill the GPU once, where one set would leave it partly idle.
+int split_to_fill(long long blocks, long long steps, long long slots) {
+    if (blocks >= slots) return 1;
+    return static_cast<int>(std::max(1LL, std::min(steps, slots / blocks)));
+}
+
+// CUDA-core pass, in tiles of 64 rows, or of 16 where that is all there are.
+Pass plan_simt(long long problems, long long R, int d, long long tiles) {
     Pass p;
-    p.blocks = problems * tiles_of(R, lard::attn::kSimtTile);
-    p.splits = 1;
-    if (p.blocks < kSms) p.splits = static_cast<int>(std::max(1LL, std::min(tiles, 2 * kSms / p.blocks)));
+    p.kind = R <= 16 ? Pass::kSimtFew : Pass::kSimt;
+    p.blocks = problems * tiles_of(R, p.kind == Pass::kSimtFew ? 16 : lard::attn::kSimtTile);
+    p.splits = split_to_fill(p.blocks, tiles, simt_slots(d));
     return p;
 }
 
@@ -341,20 +351,17 @@ FwdPlan plan_fwd(const Fwd& f) {
     p.d = f.d;
     p.rows = static_cast<long long>(f.B) * f.Hkv * f.group_rows();
     const long long own = static_cast<long long>(f.B) * f.Hkv;
-    if (f.dtype == LARD_DTYPE_FP32) {
-        long long tiles = 0;
-        for (int s = 0; s < f.nseg; ++s) tiles += tiles_of(f.seg[s].rows, lard::attn::kSimtTile);
-        p.pass[p.npass++] = plan_simt(own, f.group_rows(), tiles);
-        return p;
-    }
-    auto tc_or_few = [&](int seg, int nseg, bool shared) {
+    const bool fp32 = f.dtype == LARD_DTYPE_FP32;
+    auto add = [&](int seg, int nseg, bool shared) {
         const long long problems = shared ? f.Hkv : own, R = f.group_rows() * (shared ? f.B : 1);
-        long long tiles = 0, groups = 0;
-        for (int s = seg; s < seg + nseg; ++s) {
-            tiles += tiles_of(f.seg[s].rows, 128);
-            groups += tiles_of(f.seg[s].rows, 16);
-        }
-        Pass x = R <= lard::attn::kFewRows ? plan_few(problems, groups, f.d) : plan_tc(problems, R, f.d, tiles, p.rows);
+        auto tiles = [&](int tile) {
+            long long t = 0;
+            for (int s = seg; s < seg + nseg; ++s) t += tiles_of(f.seg[s].rows, tile);
+            return t;
+        };
+        Pass x = fp32                         ? plan_simt(problems, R, f.d, tiles(lard::attn::kSimtTile))
+                 : R <= lard::attn::kFewRows ? plan_few(problems, tiles(16), f.d)
+                                              : plan_tc(problems, R, f.d, tiles(128), p.rows);
         x.seg = seg;
         x.nseg = nseg;
         x.shared = shared;
@@ -364,12 +371,12 @@ FwdPlan plan_fwd(const Fwd& f) {
     // there is one sequence, or so little to read again (from L2) that a pass and a join
     // cost more: they take about 7 us, in which L2 brings some 16 MB to blocks
     // that wait for them.
-    const double again = static_cast<double>(f.B) * f.Hkv * f.seg[0].rows * f.d * 4.0;
+    const double again = static_cast<double>(f.B) * f.Hkv * f.seg[0].rows * f.d * 2.0 * elem_bytes(f.dtype);
     if (f.nseg == 2 && f.B > 1 && !(f.group_rows() <= lard::attn::kFewRows && again <= 16.0e6)) {
-        tc_or_few(0, 1, true);
-        tc_or_few(1, 1, false);
+        add(0, 1, true);
+        add(1, 1, false);
     } else {
-        tc_or_few(0, f.nseg, f.nseg == 1 && f.B > 1 && f.seg[0].shared);
+        add(0, f.nseg, f.nseg == 1 && f.B > 1 && f.seg[0].shared);
     }
     return p;
 }
@@ -405,7 +412,6 @@ FwdArgs<T> fwd_args(const Fwd& f) {
         g.seg[s] = KeySeg<T>{view<const T>(x.k), view<const T>(x.v), x.len, x.rows, x.causal};
     }
     g.nseg = f.nseg;
-    g.B = f.B;
     g.Hkv = f.Hkv;
     g.G = f.Hq / f.Hkv;
     g.n = f.n;
@@ -414,8 +420,8 @@ FwdArgs<T> fwd_args(const Fwd& f) {
 }
 
 // What the passes' arguments have in common.
-template <typename A>
-void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<bf16>& g) {
+template <typename A, typename T>
+void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<T>& g) {
     a.q = g.q;
     a.out = g.out;
     a.lse = g.lse;
@@ -425,12 +431,29 @@ void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, 
     a.G = g.G;
     a.n = g.n;
     a.R = static_cast<int>(f.group_rows() * (x.shared ? f.B : 1));
+    a.splits = x.splits;
     a.split0 = split0;
     a.join = p.join();
     a.rows = p.rows;
     a.part_o = g.part_o;
     a.part_lse = g.part_lse;
     a.cfac = g.cfac;
+}
+
+template <int D>
+lard_status run_simt(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<float>& g,
+                     cudaStream_t stream) {
+    using namespace lard::attn;
+    FwdArgs<float> a;
+    pass_args(a, f, p, x, split0, g);
+    a.seg[0] = g.seg[x.seg];
+    a.seg[1] = g.seg[x.nseg > 1 ? x.seg + 1 : x.seg];
+    const unsigned grid = static_cast<unsigned>(x.blocks * x.splits);
+    if (x.kind == Pass::kSimtFew)
+        attn_fwd_simt_kernel<D, 2><<<grid, kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(a);
+    else
+        attn_fwd_simt_kernel<D, 8><<<grid, kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(a);
+    return LARD_OK;
 }
 
 // The key segments of a pass for TMA loads of box_rows rows.
@@ -461,7 +484,6 @@ lard_status run_few(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, c
     pass_args(a, f, p, x, split0, g);
     if (!make_segs(a.seg, f, x, 16)) return LARD_ERR_INVALID_ARG;
     a.cluster = x.cluster;
-    a.splits = x.splits;
     a.wait_ns = kWaitLimitNs;
     a.drain_ns = kDrainLimitNs;
     cudaLaunchConfig_t c = {};
@@ -485,7 +507,6 @@ lard_status run_tc(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, co
     TcFwdArgs a;
     pass_args(a, f, p, x, split0, g);
     if (!make_segs(a.seg, f, x, 128)) return LARD_ERR_INVALID_ARG;
-    a.splits = x.splits;
     a.wait_ns = kWaitLimitNs;
     a.drain_ns = kDrainLimitNs;
     const unsigned grid = static_cast<unsigned>(x.blocks * x.splits);
@@ -501,19 +522,18 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
     using namespace lard::attn;
     FwdArgs<T> g = fwd_args<T>(f);
     g.splits = p.partials();
+    g.rows = p.rows;
     g.part_o = static_cast<float*>(ws);
     g.part_lse = reinterpret_cast<float*>(static_cast<char*>(ws) + p.part_o());
-    if constexpr (std::is_same<T, float>::value) {
-        attn_fwd_simt_kernel<T, D>
-            <<<static_cast<unsigned>(p.pass[0].blocks * p.pass[0].splits), kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(g);
-    } else {
-        int split0 = 0;
-        for (int k = 0; k < p.npass; ++k) {
-            const lard_status st = p.pass[k].kind == Pass::kFew ? run_few<D>(f, p, p.pass[k], split0, g, stream)
-                                                                : run_tc<D>(f, p, p.pass[k], split0, g, stream);
-            if (st != LARD_OK) return st;
-            split0 += p.pass[k].splits;
-        }
+    int split0 = 0;
+    for (int k = 0; k < p.npass; ++k) {
+        const Pass& x = p.pass[k];
+        lard_status st = LARD_OK;
+        if constexpr (std::is_same<T, float>::value) st = run_simt<D>(f, p, x, split0, g, stream);
+        else if (x.kind == Pass::kFew) st = run_few<D>(f, p, x, split0, g, stream);
+        else st = run_tc<D>(f, p, x, split0, g, stream);
+        if (st != LARD_OK) return st;
+        split0 += x.splits;
     }
     if (p.join())
         attn_join_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.rows, kJoinRowsPerBlock)), 256, 0, stream>>>(g);
@@ -577,10 +597,7 @@ lard_status cross_sizes(const lard_cross_attn* a) {
     lard_status st = check_sizes(a->dtype, a->B, a->Hq, a->Hkv, a->n, a->d, a->tau);
     if (st != LARD_OK) return st;
     if (a->m < 1 || a->m > kMaxRows) return LARD_ERR_INVALID_ARG;
-    if (!plan_fwd(cross_work(*a)).grids_fit() ||
-        static_cast<long long>(a->B) * a->Hkv * tiles_of(a->m, lard::attn::kSimtTile) > INT_MAX)
-        return LARD_ERR_INVALID_ARG;
-    return LARD_OK;
+    return plan_fwd(cross_work(*a)).grids_fit() ? LARD_OK : LARD_ERR_INVALID_ARG;
 }
 
 lard_status prefix_sizes(const lard_prefix_attn_args* a) {
@@ -604,12 +621,44 @@ lard_status launch_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t st
 }
 
 // ------------------------------------------------------------------ backward
-size_t bwd_bytes(const lard_cross_attn& a) {
-    return (static_cast<size_t>(a.B) * a.Hq * a.n * 4 + 15) / 16 * 16;  // delta
+// Layout of a backward call: splits of the key axis for dQ and of the row axis
+// for dK and dV, and the workspace: delta, then the partial sums.
+struct BwdPlan {
+    long long qblocks = 0, kblocks = 0;  // of one split
+    int qsplits = 1, ksplits = 1;
+    size_t delta = 0, part_q = 0, part_kv = 0;  // bytes; part_kv of dK and of dV each
+    long long sum_rows = 0;
+    size_t bytes() const { return delta + part_q + 2 * part_kv; }
+    bool grids_fit() const {
+        return qblocks * qsplits <= INT_MAX && kblocks * ksplits <= INT_MAX && tiles_of(sum_rows, kJoinRowsPerBlock) <= INT_MAX;
+    }
+};
+
+BwdPlan plan_bwd(const lard_cross_attn& a) {
+    BwdPlan p;
+    const long long BH = static_cast<long long>(a.B) * a.Hkv, R = static_cast<long long>(a.Hq / a.Hkv) * a.n;
+    p.delta = (static_cast<size_t>(BH) * R * 4 + 15) / 16 * 16;
+    const int tile = a.dtype == LARD_DTYPE_FP32 ? lard::attn::kSimtTile : 128;
+    p.qblocks = BH * tiles_of(R, tile);
+    p.kblocks = BH * tiles_of(a.m, tile);
+    if (a.dtype == LARD_DTYPE_FP32) {
+        p.qsplits = split_to_fill(p.qblocks, tiles_of(a.m, tile), simt_slots(a.d));
+        p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), kSms);
+    }
+    if (p.qsplits > 1) {
+        p.part_q = static_cast<size_t>(p.qsplits) * BH * R * a.d * 4;
+        p.sum_rows += BH * R;
+    }
+    if (p.ksplits > 1) {
+        p.part_kv = static_cast<size_t>(p.ksplits) * BH * a.m * a.d * 4;
+        p.sum_rows += 2 * BH * a.m;
+    }
+    return p;
 }
 
 template <int D>
-lard_status run_bwd_tc(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+                       cudaStream_t stream) {
     using namespace lard::attn;
     TcBwdArgs g;
     if (!make_map(&g.k, v[1], a.B, a.Hkv, a.m, D) || !make_map(&g.v, v[2], a.B, a.Hkv, a.m, D) ||
@@ -641,49 +690,71 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const lard_attn_view (&v)[8], v
     g.tau = a.tau;
     g.wait_ns = kWaitLimitNs;
     g.drain_ns = kDrainLimitNs;
-    const long long BH = static_cast<long long>(a.B) * a.Hkv, R = static_cast<long long>(g.G) * a.n;
-    attn_dq_tc_kernel<D>
-        <<<static_cast<unsigned>(BH * tiles_of(R, 128)), kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream>>>(g);
-    attn_dkdv_tc_kernel<D>
-        <<<static_cast<unsigned>(BH * tiles_of(a.m, 128)), kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream>>>(g);
+    attn_dq_tc_kernel<D><<<static_cast<unsigned>(p.qblocks), kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream>>>(g);
+    attn_dkdv_tc_kernel<D><<<static_cast<unsigned>(p.kblocks), kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream>>>(g);
     return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
 }
 
-template <int D>
-lard_status run_bwd_simt(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+// Adds the partial sums that a backward call left.
+template <typename T, int D>
+void run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
+              const float* part_k, const float* part_v, cudaStream_t stream) {
     using namespace lard::attn;
-    using T = float;
-    BwdArgs<T> g;
-    g.q = view<const T>(v[0]);
-    g.k = view<const T>(v[1]);
-    g.v = view<const T>(v[2]);
-    g.out = view<const T>(v[3]);
-    g.dout = view<const T>(v[4]);
-    g.dq = view<T>(v[5]);
-    g.dk = view<T>(v[6]);
-    g.dv = view<T>(v[7]);
+    if (p.sum_rows == 0) return;
+    SumArgs<T> s;
+    s.jobs = 0;
+    if (p.qsplits > 1)
+        s.job[s.jobs++] = {part_q, view<T>(v[5]), p.qsplits, a.Hq, a.n, static_cast<long long>(a.B) * a.Hq * a.n, a.tau};
+    if (p.ksplits > 1) {
+        const long long rows = static_cast<long long>(a.B) * a.Hkv * a.m;
+        s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, rows, a.tau};
+        s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, rows, 1.f};
+    }
+    attn_sum_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.sum_rows, kJoinRowsPerBlock)), 256, 0, stream>>>(s);
+}
+
+template <int D>
+lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+                         cudaStream_t stream) {
+    using namespace lard::attn;
+    SimtBwdArgs g;
+    g.q = view<const float>(v[0]);
+    g.k = view<const float>(v[1]);
+    g.v = view<const float>(v[2]);
+    g.out = view<const float>(v[3]);
+    g.dout = view<const float>(v[4]);
+    g.dq = view<float>(v[5]);
+    g.dk = view<float>(v[6]);
+    g.dv = view<float>(v[7]);
     g.lse = a.lse;
-    g.delta = static_cast<float*>(ws);
+    char* w = static_cast<char*>(ws);
+    g.delta = reinterpret_cast<float*>(w);
+    g.part_q = reinterpret_cast<float*>(w + p.delta);
+    g.part_k = reinterpret_cast<float*>(w + p.delta + p.part_q);
+    g.part_v = reinterpret_cast<float*>(w + p.delta + p.part_q + p.part_kv);
     g.len = a.k_len;
     g.m = a.m;
     g.B = a.B;
     g.Hkv = a.Hkv;
     g.G = a.Hq / a.Hkv;
     g.n = a.n;
+    g.qsplits = p.qsplits;
+    g.ksplits = p.ksplits;
     g.cfac = log2_factor(a.tau);
     g.tau = a.tau;
-    const long long BH = static_cast<long long>(a.B) * a.Hkv, R = static_cast<long long>(g.G) * a.n;
-    const long long rtiles = (R + kSimtTile - 1) / kSimtTile;
-    attn_delta_kernel<T, D><<<static_cast<unsigned>((BH * R + 7) / 8), 256, 0, stream>>>(g);
-    attn_dkdv_simt_kernel<T, D><<<static_cast<unsigned>(BH * tiles_of(a.m, kSimtTile)), kSimtThreads, SimtLayout<D>::BWD_BYTES, stream>>>(g);
-    attn_dq_simt_kernel<T, D><<<static_cast<unsigned>(BH * rtiles), kSimtThreads, SimtLayout<D>::BWD_BYTES, stream>>>(g);
+    attn_dq_simt_kernel<D>
+        <<<static_cast<unsigned>(p.qblocks * p.qsplits), kSimtThreads, SimtLayout<D>::DQ_BYTES, stream>>>(g);
+    attn_dkdv_simt_kernel<D>
+        <<<static_cast<unsigned>(p.kblocks * p.ksplits), kSimtThreads, SimtLayout<D>::DKDV_BYTES, stream>>>(g);
+    run_sums<float, D>(a, p, v, g.part_q, g.part_k, g.part_v, stream);
     return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
 }
 
-lard_status launch_bwd(const lard_cross_attn& a, const lard_attn_view (&v)[8], void* ws, cudaStream_t stream) {
+lard_status launch_bwd(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+                       cudaStream_t stream) {
     if (a.dtype == LARD_DTYPE_BF16)
-        return a.d == 64 ? run_bwd_tc<64>(a, v, ws, stream) : run_bwd_tc<128>(a, v, ws, stream);
-    return a.d == 64 ? run_bwd_simt<64>(a, v, ws, stream) : run_bwd_simt<128>(a, v, ws, stream);
+        return a.d == 64 ? run_bwd_tc<64>(a, p, v, ws, stream) : run_bwd_tc<128>(a, p, v, ws, stream);
+    return a.d == 64 ? run_bwd_simt<64>(a, p, v, ws, stream) : run_bwd_simt<128>(a, p, v, ws, stream);
 }
 
 }  // namespace
@@ -695,7 +766,7 @@ size_t lard_cross_attn_fwd_workspace_bytes(const lard_cross_attn* a) {
 }
 
 size_t lard_cross_attn_bwd_workspace_bytes(const lard_cross_attn* a) {
-    return cross_sizes(a) == LARD_OK ? bwd_bytes(*a) : 0;
+    return cross_sizes(a) == LARD_OK && plan_bwd(*a).grids_fit() ? plan_bwd(*a).bytes() : 0;
 }
 
 size_t lard_prefix_attn_workspace_bytes(const lard_prefix_attn_args* a) {
@@ -748,7 +819,9 @@ lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_
         !bufs.add_view(a->dv, a->B, a->Hkv, a->m, a->d, e, true, &v[7]))
         return LARD_ERR_INVALID_ARG;
     if (!a->lse || !aligned(a->lse, 4) || (a->k_len && !aligned(a->k_len, 4))) return LARD_ERR_INVALID_ARG;
-    const size_t need = bwd_bytes(*a);
+    const BwdPlan plan = plan_bwd(*a);
+    if (!plan.grids_fit()) return LARD_ERR_INVALID_ARG;
+    const size_t need = plan.bytes();
     if (!workspace_ok(workspace, workspace_bytes, need)) return LARD_ERR_INVALID_ARG;
     bufs.add_flat(a->lse, static_cast<size_t>(a->B) * a->Hq * a->n * 4, false);
     bufs.add_flat(a->k_len, static_cast<size_t>(a->B) * 4, false);
@@ -757,7 +830,7 @@ lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_
     DeviceGuard guard;
     st = bufs.select_device();
     if (st != LARD_OK) return st;
-    return launch_bwd(*a, v, workspace, stream);
+    return launch_bwd(*a, plan, v, workspace, stream);
 }
 
 lard_status lard_prefix_attn(const lard_prefix_attn_args* a, void* workspace, size_t workspace_bytes,
