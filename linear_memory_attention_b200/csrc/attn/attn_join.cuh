@@ -9,7 +9,7 @@ namespace lard {
 namespace attn {
 
 // Joins the splits of a row: LSE = log sum_s exp LSE_s, O = sum_s exp(LSE_s - LSE) O_s.
-// One warp per row; lanes share the head dimension.
+// One warp per row; lanes share the splits' weights, then the head dimension.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs<T> g) {
     const int lane = threadIdx.x & 31;
@@ -24,13 +24,26 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     float total = 0.f, o[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int s = 0; s < g.splits; ++s) {
-        const float w = exp2f((g.part_lse[s * g.rows + row] - base) * kLog2e);
-        total += w;
-        if (w == 0.f) continue;  // a split that saw nothing need not have written its O
-        const float* src = g.part_o + (s * g.rows + row) * D + lane * E;
+    for (int s0 = 0; s0 < g.splits; s0 += 32) {
+        const int here = min(32, g.splits - s0);
+        const float mine = lane < here ? exp2f((g.part_lse[(s0 + lane) * g.rows + row] - base) * kLog2e) : 0.f;
+#pragma unroll 8
+        for (int s = 0; s < here; ++s) {
+            const float w = __shfl_sync(0xffffffffu, mine, s);
+            total += w;
+            // A split that saw nothing need not have written its O.
+            const float* src = g.part_o + ((w == 0.f ? 0 : s0 + s) * g.rows + row) * D + lane * E;
+            float x[E];
+            if constexpr (E == 4) {
+                const float4 v = load4(src);
+                x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(src);
+                x[0] = v.x; x[1] = v.y;
+            }
 #pragma unroll
-        for (int e = 0; e < E; ++e) o[e] = fmaf(w, src[e], o[e]);
+            for (int e = 0; e < E; ++e) o[e] = w == 0.f ? o[e] : fmaf(w, x[e], o[e]);
+        }
     }
     const float inv = total == 0.f ? 0.f : 1.f / total;
     const int R = g.G * g.n;

@@ -262,7 +262,7 @@ Pass plan_simt(long long problems, long long R, int d, long long tiles) {
     Pass p;
     p.kind = R <= 16 ? Pass::kSimtFew : Pass::kSimt;
     p.blocks = problems * tiles_of(R, p.kind == Pass::kSimtFew ? 16 : lard::attn::kSimtTile);
-    p.splits = split_to_fill(p.blocks, tiles, simt_slots(d));
+    p.splits = split_to_fill(p.blocks, tiles_of(tiles, 2), simt_slots(d));  // two tiles at a time
     return p;
 }
 
@@ -643,7 +643,7 @@ BwdPlan plan_bwd(const lard_cross_attn& a) {
     p.kblocks = BH * tiles_of(a.m, tile);
     if (a.dtype == LARD_DTYPE_FP32) {
         p.qsplits = split_to_fill(p.qblocks, tiles_of(a.m, tile), simt_slots(a.d));
-        p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), kSms);
+        p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), simt_slots(a.d));
     }
     if (p.qsplits > 1) {
         p.part_q = static_cast<size_t>(p.qsplits) * BH * R * a.d * 4;
