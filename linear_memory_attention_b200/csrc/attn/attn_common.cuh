@@ -76,5 +76,64 @@ __device__ __forceinline__ int causal_limit(int len, int n, int i) {
     return e < 0 ? 0 : (e > len ? len : static_cast<int>(e));
 }
 
+// 16 bytes from global to shared memory, or zeros.
+__device__ __forceinline__ void copy16_or_0(uint32_t dst, const void* src, bool in) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// The pointer that lane `from` holds.
+template <typename T>
+__device__ __forceinline__ T* shfl_ptr(T* p, int from) {
+    return reinterpret_cast<T*>(__shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(p), from));
+}
+
+// A warp brings rows [first, last) of its 32 rows of D bf16 to shared memory, as
+// K-major operand rows (64-column chunks 16 KB apart, 128-byte rows, 128-byte
+// swizzle) from row0 on.  Lane r holds row r's address, or NULL for zeros.
+// Neighbouring lanes read neighbouring pieces of a row: one row a lane would
+// touch 32 rows with every instruction.
+template <int D>
+__device__ __forceinline__ void rows_to_operand(uint32_t tile, int row0, const __nv_bfloat16* mine, int lane, int first,
+                                                int last) {
+    constexpr int kLanes = D / 8;  // lanes of a row
+#pragma unroll 4
+    for (int k = first; k < last; k += 32 / kLanes) {
+        const int r = k + lane / kLanes, u = lane % kLanes;
+        const __nv_bfloat16* src = shfl_ptr(mine, r);
+        const int row = row0 + r;
+        copy16_or_0(tile + (u >> 3) * 16384 + row * 128 + (((u & 7) ^ (row & 7)) << 4), src ? src + u * 8 : nullptr, src);
+    }
+}
+
+// A warp writes its 32 rows of ROW bytes from a staging area of its own (32 ROW
+// bytes of shared memory) to global memory.  Lane r has put row r's 16-byte
+// units at stage_unit(r, u) and holds its address, or NULL to skip it.
+template <int ROW>
+__device__ __forceinline__ uint32_t stage_unit(uint32_t stage, int r, int u) {
+    return stage + r * ROW + ((u ^ (r & 7)) << 4);
+}
+template <int ROW>
+__device__ __forceinline__ void staged_rows_out(uint32_t stage, void* mine, int lane) {
+    constexpr int kLanes = ROW / 16;  // lanes of a row
+    __syncwarp();
+#pragma unroll 4
+    for (int k = 0; k < 32; k += 32 / kLanes) {
+        const int r = k + lane / kLanes, u = lane % kLanes;
+        char* dst = shfl_ptr(static_cast<char*>(mine), r);
+        uint4 x;
+        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w)
+                     : "r"(stage_unit<ROW>(stage, r, u))
+                     : "memory");
+        if (dst) *reinterpret_cast<uint4*>(dst + u * 16) = x;
+    }
+    __syncwarp();  // the area may be written again
+}
+
 }  // namespace attn
 }  // namespace lard

@@ -301,23 +301,15 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         const int Gn = g.G * g.n;
         const int b = pb + (row_ok ? r / Gn : 0), rem = row_ok ? r % Gn : 0;
         const int head = hk * g.G + rem / g.n, pos = rem % g.n;
-        // Q into shared memory, rows past the end as zeros; by keys each
-        // stream writes half of the one tile's columns.
-        {
-            const uint4* src = reinterpret_cast<const uint4*>(g.q.row(b, head, pos));
-            const uint32_t dst = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE) + row * 128;
-            constexpr int kUnits = D / 8;
-#pragma unroll
-            for (int e = 0; e < (kByKeys ? kUnits / 2 : kUnits); ++e) {
-                const int u = kByKeys ? i * (kUnits / 2) + e : e;
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (row_ok) x = __ldg(src + u);
-                ptx::st_shared_v4(dst + (u >> 3) * 16384 + (((u & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
-            }
-            ptx::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(&ctrl->q_ready);
-        }
+        // Q into shared memory, rows past the end as zeros; by keys the two streams
+        // share one tile and the work.
+        rows_to_operand<D>(ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE), q4 * 32,
+                           row_ok ? g.q.row(b, head, pos) : nullptr, lane, kByKeys ? 16 * i : 0, kByKeys ? 16 * i + 16 : 32);
+        copy_commit();
+        copy_wait<0>();
+        ptx::fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) ptx::mbar_arrive(&ctrl->q_ready);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
         const float cf = g.cfac;
@@ -444,6 +436,8 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             const long long grow = (static_cast<long long>(b) * g.Hkv + hk) * Gn + rem;
             const long long prow = (g.split0 + split) * g.rows + grow;
             const bool second = kByKeys && steps(1) > 0;
+            // Through this warp's rows of Q's tile, which the last S has read, to memory.
+            const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE) + q4 * (L::TILE / 4);
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
                 float o[32];
@@ -461,18 +455,21 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(c + k) * 128 + row], w1, o[k]);
                 }
-                if (row_ok && g.join) {
-                    float* dst = g.part_o + prow * D + c;
+                if (g.join) {  // 32 columns of fp32
+                    const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
 #pragma unroll
-                    for (int k = 0; k < 32; k += 4) store4(dst + k, make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]));
-                } else if (row_ok) {
-                    uint4* dst = reinterpret_cast<uint4*>(g.out.row(b, head, pos) + c);
+                    for (int u = 0; u < 8; ++u)
+                        ptx::st_shared_v4(stage_unit<128>(area, lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
+                    staged_rows_out<128>(area, row_ok ? g.part_o + prow * D + c : nullptr, lane);
+                } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        dst[k] = make_uint4(ptx::pack_bf16x2(o[8 * k], o[8 * k + 1]), ptx::pack_bf16x2(o[8 * k + 2], o[8 * k + 3]),
-                                            ptx::pack_bf16x2(o[8 * k + 4], o[8 * k + 5]), ptx::pack_bf16x2(o[8 * k + 6], o[8 * k + 7]));
+                    for (int u = 0; u < 4; ++u)
+                        ptx::st_shared_v4(stage_unit<D * 2>(area, lane, c / 8 + u), ptx::pack_bf16x2(o[8 * u], o[8 * u + 1]),
+                                          ptx::pack_bf16x2(o[8 * u + 2], o[8 * u + 3]), ptx::pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
+                                          ptx::pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
                 }
             }
+            if (!g.join) staged_rows_out<D * 2>(area, row_ok ? g.out.row(b, head, pos) : nullptr, lane);
             if (row_ok) {
                 if (g.join) g.part_lse[prow] = lse;
                 else g.lse[grow] = lse;

@@ -40,16 +40,6 @@ struct SimtLayout {
     static_assert(FWD_BYTES <= 232448, "too much shared memory");
 };
 
-// 16 bytes from global to shared memory, or zeros.
-__device__ __forceinline__ void copy16_or_0(uint32_t dst, const void* src, bool in) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // Requests rows [0, valid) of a tile of ROWS rows and zeros behind; row(t) gives row t's address.
 // THREADS threads take part, `me` the number of each.
 template <int D, int ROWS, int THREADS, typename RowFn>

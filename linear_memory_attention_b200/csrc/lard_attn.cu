@@ -706,9 +706,9 @@ void run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (
     if (p.qsplits > 1)
         s.job[s.jobs++] = {part_q, view<T>(v[5]), p.qsplits, a.Hq, a.n, static_cast<long long>(a.B) * a.Hq * a.n, a.tau};
     if (p.ksplits > 1) {
-        const long long rows = static_cast<long long>(a.B) * a.Hkv * a.m;
-        s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, rows, a.tau};
-        s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, rows, 1.f};
+        const long long keys = static_cast<long long>(a.B) * a.Hkv * a.m;
+        s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, keys, a.tau};
+        s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, keys, 1.f};
     }
     attn_sum_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.sum_rows, kJoinRowsPerBlock)), 256, 0, stream>>>(s);
 }
