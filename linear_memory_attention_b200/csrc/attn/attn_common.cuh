@@ -115,7 +115,8 @@ __device__ __forceinline__ void rows_to_operand(uint32_t tile, int row0, const _
 // units at stage_unit(r, u) and holds its address, or NULL to skip it.
 template <int ROW>
 __device__ __forceinline__ uint32_t stage_unit(uint32_t stage, int r, int u) {
-    return stage + r * ROW + ((u ^ (r & 7)) << 4);
+    // Eight lanes in a row (rows when writing, units when reading) use different banks.
+    return stage + r * ROW + ((u ^ (ROW >= 128 ? r & 7 : r >> 1 & 3)) << 4);
 }
 template <int ROW>
 __device__ __forceinline__ void staged_rows_out(uint32_t stage, void* mine, int lane) {

@@ -78,7 +78,7 @@ struct FwdTcLayout {
 
 struct FwdTcCtrl {
     uint64_t kv_full[10], kv_empty[10];
-    uint64_t q_ready, mma_done;
+    uint64_t q_ready, tail_ready, mma_done;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
     int abort_flag;
@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     // Segment and first key of a tile.
     auto seg_of = [&](int tile) { return tile < tiles0 ? 0 : 1; };
     auto key_of = [&](int tile) { return (tile < tiles0 ? tile : tile - tiles0) * 128; };
+    auto is_tail = [&](int tile) { return (tile < tiles0 ? len0 : len1) - key_of(tile) < 128; };
     constexpr int kTiles = kByKeys ? 2 : 1;  // K (and V) tiles of a step
 
     if (threadIdx.x == 0) {
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             ptx::mbar_init(&ctrl->kv_empty[s], 1);
         }
         ptx::mbar_init(&ctrl->q_ready, 8);
+        ptx::mbar_init(&ctrl->tail_ready, 1);
         ptx::mbar_init(&ctrl->mma_done, 1);
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(&ctrl->s_full[i], 1);
@@ -170,7 +172,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                 const int i = u % kTiles;
                 const bool is_v = u >= kTiles;
                 if (kByKeys && t >= steps(i)) continue;
-                ok = ptx::mbar_wait(&ctrl->kv_empty[slot], (round & 1) ^ 1, abort_flag, lim, &g_lard_fault,
+                ok = mbar_wait(&ctrl->kv_empty[slot], (round & 1) ^ 1, abort_flag, lim, &g_lard_fault,
                                     kFaultFwdProducer);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
@@ -186,6 +188,19 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                 }
                 __syncwarp();
                 ++issued;
+                if (is_v && is_tail(tile_of(t, i))) {  // values past the sequence's end: zeros
+                    const int tile = tile_of(t, i);
+                    ok = mbar_wait(&ctrl->kv_full[slot], round & 1, abort_flag, lim, &g_lard_fault, kFaultFwdProducer);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    uint8_t* v = smem + L::OFF_KV + slot * L::TILE;
+                    for (int e = ((seg_of(tile) ? len1 : len0) - key_of(tile)) * 8 + lane; e < 1024; e += 32)
+                        for (int c = 0; c < L::KC; ++c)
+                            *reinterpret_cast<uint4*>(v + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ptx::mbar_arrive(&ctrl->tail_ready);
+                }
                 if (++slot == L::NS) { slot = 0; ++round; }
             }
         }
@@ -196,99 +211,105 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         }
       } else if (warp == 1) {
         // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t kIdescO = ptx::idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kHi = ptx::sdesc_hi(1024);
-        const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_Q), 16);
-        const uint32_t kv_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16);
-        const uint32_t kv_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16384);
-        // Ring slot of a step's K or V tile; all steps but the last have 2 * kTiles slots.
-        auto index_of = [&](int t, int u) {
-            if (kByKeys && t == S - 1 && steps(1) < S) return 4 * t + (u >= 2 ? 1 : 0);
-            return 2 * kTiles * t + u;
-        };
-        auto wait_slot = [&](int idx) {
-            const bool ok = ptx::mbar_wait(&ctrl->kv_full[idx % L::NS], (idx / L::NS) & 1, abort_flag, lim,
-                                           &g_lard_fault, kFaultFwdMma);
-            return __all_sync(0xffffffffu, ok) != 0;
-        };
-        auto issue_s = [&](int i, int idx) {  // S_i = Q_i K^T; Q is one tile by keys
-            const uint32_t a = q_lo + (kByKeys ? 0 : i * (L::TILE >> 4)), b = kv_k + (idx % L::NS) * (L::TILE >> 4);
-            const uint32_t d = tmem + i * 128;
-#pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-                if (kk == 0) ptx::umma_ss<0>(d, a, b, kHi, kIdescS);
-                else ptx::umma_ss<1>(d, a + ptx::desc_step_k(kk), b + ptx::desc_step_k(kk), kHi, kIdescS);
-            }
-            ptx::umma_commit(&ctrl->s_full[i]);
-        };
-        auto issue_o = [&](int i, int idx, bool first) {  // O_i (+)= P_i V
-            const uint32_t a = tmem + i * 128, b = kv_mn + (idx % L::NS) * (L::TILE >> 4);
-            const uint32_t d = tmem + 256 + i * 128;
-            umma_ts_acc(d, a, b, kHi, kIdescO, first ? 0u : 1u);
-#pragma unroll
-            for (int kk = 1; kk < 8; ++kk) ptx::umma_ts<1>(d, a + kk * 8, b + ptx::desc_step_mn(kk), kHi, kIdescO);
-            ptx::umma_commit(&ctrl->o_full[i]);
-        };
-        bool ok = S > 0 && ptx::mbar_wait(&ctrl->q_ready, 0, abort_flag, lim, &g_lard_fault, kFaultFwdMma);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) ptx::tc_fence_after();
-        for (int i = 0; ok && i < nstream; ++i) {
-            if (steps(i) == 0) continue;
-            const int ik = index_of(0, kByKeys ? i : 0);
-            ok = wait_slot(ik);
-            if (!ok) break;
-            if (lane == 0) {
-                issue_s(i, ik);
-                if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[ik % L::NS]);
-            }
-            __syncwarp();
-        }
-        for (int t = 0; ok && t < S; ++t) {
-            for (int i = 0; ok && i < nstream; ++i) {
-                if (t >= steps(i)) continue;
-                const int iv = index_of(t, kTiles + (kByKeys ? i : 0));
-                if (kByKeys || i == 0) {
-                    ok = wait_slot(iv);
-                    if (!ok) break;
-                    // Rows past the sequence's end inside its last tile.
-                    const int tile = tile_of(t, i);
-                    const int valid = (seg_of(tile) ? len1 : len0) - key_of(tile);
-                    if (valid < 128) {
-                        uint8_t* v = smem + L::OFF_KV + (iv % L::NS) * L::TILE;
-                        for (int e = valid * 8 + lane; e < 1024; e += 32)
-                            for (int c = 0; c < L::KC; ++c)
-                                *reinterpret_cast<uint4*>(v + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
-                        ptx::fence_proxy_async_smem();
-                        __syncwarp();
+        // One thread, and little else in its loop than waits and products: what
+        // it does between them, the tensor pipe waits for.
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t kIdescO = ptx::idesc_bf16(128, D, 0, 1);
+            constexpr uint32_t kHi = ptx::sdesc_hi(1024);
+            const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_Q), 16);
+            const uint32_t kv_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16);
+            const uint32_t kv_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_KV), 16384);
+            // A place in the ring and the parity of its round.
+            struct Place {
+                int slot, parity;
+                __device__ __forceinline__ void advance(int n) {
+                    slot += n;
+                    if (slot >= L::NS) {
+                        slot -= L::NS;
+                        parity ^= 1;
                     }
                 }
-                ok = ptx::mbar_wait(&ctrl->p_full[i], t & 1, abort_flag, lim, &g_lard_fault, kFaultFwdMma);
-                ok = __all_sync(0xffffffffu, ok);
+            };
+            auto wait = [&](uint64_t* bar, int parity) {
+                return mbar_wait(bar, parity, abort_flag, lim, &g_lard_fault, kFaultFwdMma);
+            };
+            auto wait_place = [&](const Place& x) { return wait(&ctrl->kv_full[x.slot], x.parity); };
+            auto release = [&](const Place& x) { ptx::umma_commit(&ctrl->kv_empty[x.slot]); };
+            auto issue_s = [&](int i, const Place& x) {  // S_i = Q_i K^T; Q is one tile by keys
+                const uint32_t a = q_lo + (kByKeys ? 0 : i * (L::TILE >> 4));
+                const uint32_t b = kv_k + x.slot * (L::TILE >> 4);
+                const uint32_t d = tmem + i * 128;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    if (kk == 0) ptx::umma_ss<0>(d, a, b, kHi, kIdescS);
+                    else ptx::umma_ss<1>(d, a + ptx::desc_step_k(kk), b + ptx::desc_step_k(kk), kHi, kIdescS);
+                }
+                ptx::umma_commit(&ctrl->s_full[i]);
+            };
+            auto issue_o = [&](int i, const Place& x, bool first) {  // O_i (+)= P_i V
+                const uint32_t a = tmem + i * 128, b = kv_mn + x.slot * (L::TILE >> 4);
+                const uint32_t d = tmem + 256 + i * 128;
+                umma_ts_acc(d, a, b, kHi, kIdescO, first ? 0u : 1u);
+#pragma unroll
+                for (int kk = 1; kk < 8; ++kk) ptx::umma_ts<1>(d, a + kk * 8, b + ptx::desc_step_mn(kk), kHi, kIdescO);
+                ptx::umma_commit(&ctrl->o_full[i]);
+            };
+            // Ring order: step by step the K tiles, then the V tiles; by keys an
+            // odd last step has one of each.
+            Place k[2] = {{0, 0}, {kByKeys ? 1 : 0, 0}}, v[2] = {{kTiles, 0}, {2 * kTiles - 1, 0}};
+            const int steps1 = steps(1);
+            bool ok = S > 0 && wait(&ctrl->q_ready, 0);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (!ok || (i == 1 && steps1 == 0)) break;
+                if (kByKeys || i == 0) ok = wait_place(k[i]);
                 if (!ok) break;
-                ptx::tc_fence_after();
-                if (lane == 0) {
-                    issue_o(i, iv, t == 0);
-                    if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[iv % L::NS]);
-                }
-                __syncwarp();
-                if (t + 1 < steps(i)) {  // behind O_i, whose P lies where S_i goes
-                    const int ik = index_of(t + 1, kByKeys ? i : 0);
-                    if (kByKeys || i == 0) {
-                        ok = wait_slot(ik);
-                        if (!ok) break;
-                    }
-                    if (lane == 0) {
-                        issue_s(i, ik);
-                        if (kByKeys || i == nstream - 1) ptx::umma_commit(&ctrl->kv_empty[ik % L::NS]);
-                    }
-                    __syncwarp();
-                }
+                issue_s(i, k[i]);
+                if (kByKeys || i == nstream - 1) release(k[i]);
             }
+            int tails = 0;
+            for (int t = 0; ok && t < S; ++t) {
+                const bool both = t < steps1;                  // stream 1 takes part in this step,
+                const bool more0 = t + 1 < S, more1 = t + 1 < steps1;  // and either in the next
+                if (kByKeys && !both) {
+                    v[0] = k[0];
+                    v[0].advance(1);
+                }
+                Place kn[2] = {k[0], k[1]};
+                kn[0].advance(2 * kTiles);
+                if (kByKeys) kn[1].advance(2 * kTiles);
+                else kn[1] = kn[0];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    if (i == 1 && !both) continue;
+                    const bool last = kByKeys || i == 1 || !both;  // stream to use a tile
+                    if (kByKeys || i == 0) {
+                        ok = ok && wait_place(v[i]);
+                        // Rows past a sequence's end: the producer makes them zeros.
+                        if (ok && is_tail(tile_of(t, i))) ok = wait(&ctrl->tail_ready, tails++ & 1);
+                    }
+                    ok = ok && wait(&ctrl->p_full[i], t & 1);
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    issue_o(i, v[kByKeys ? i : 0], t == 0);
+                    if (last) release(v[kByKeys ? i : 0]);
+                    if (i == 0 ? more0 : more1) {  // behind the product that reads P where this S goes
+                        if (kByKeys || i == 0) ok = wait_place(kn[i]);
+                        if (!ok) break;
+                        issue_s(i, kn[i]);
+                        if (last) release(kn[i]);
+                    }
+                }
+                k[0] = kn[0];
+                k[1] = kn[1];
+                v[0].advance(2 * kTiles);
+                if (kByKeys) v[1].advance(2 * kTiles);
+            }
+            ptx::umma_commit(&ctrl->mma_done);
+            drain(&ctrl->mma_done, 0, dlim);
         }
-        if (lane == 0) ptx::umma_commit(&ctrl->mma_done);
         __syncwarp();
-        drain(&ctrl->mma_done, 0, dlim);
       }
     } else {
         ptx::regs_inc<kFwdTcRegsSoft>();
@@ -320,7 +341,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             const int tile = tile_of(t, i), s = seg_of(tile), j0 = key_of(tile);
             const int size = s ? len1 : len0;
             const int lim_keys = (g.seg[s].causal ? causal_limit(size, g.n, pos) : size) - j0;
-            ok = ptx::mbar_wait(&ctrl->s_full[i], t & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+            ok = mbar_wait(&ctrl->s_full[i], t & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
@@ -350,7 +371,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                 // O(t - 1) is complete; bring it to the new reference.
                 const float sc = rise ? ptx::ex2(m - mnew) : 1.f;
                 l *= sc;
-                ok = ptx::mbar_wait(&ctrl->o_full[i], (t - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+                ok = mbar_wait(&ctrl->o_full[i], (t - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::tc_fence_after();
@@ -392,7 +413,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         }
         // ------------------------------------------------------------ epilogue
         if (ok && mine > 0) {
-            ok = ptx::mbar_wait(&ctrl->o_full[i], (mine - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
+            ok = mbar_wait(&ctrl->o_full[i], (mine - 1) & 1, abort_flag, lim, &g_lard_fault, kFaultFwdSoftmax);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
         }

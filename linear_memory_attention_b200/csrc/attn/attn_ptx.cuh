@@ -16,6 +16,26 @@ __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* m
         : "memory");
 }
 
+// ptx::mbar_wait with the clock and the abort flag looked at once in 64 tries:
+// reading %globaltimer takes hundreds of cycles, by which each wait that does
+// not find its phase complete at once would be late.
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, uint64_t limit_ns,
+                                          unsigned int* fault_word, unsigned int code) {
+    for (int k = 0; k < 64; ++k)
+        if (ptx::mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = ptx::globaltimer_ns();
+    while (true) {
+        for (int k = 0; k < 64; ++k)
+            if (ptx::mbar_try_wait(bar, parity)) return true;
+        if (*abort_flag) return false;
+        if (ptx::globaltimer_ns() - t0 > limit_ns) {
+            *abort_flag = 1;
+            atomicOr(fault_word, code);
+            return false;
+        }
+    }
+}
+
 // umma_ts with the accumulate flag at run time.
 __device__ __forceinline__ void umma_ts_acc(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t hi, uint32_t idesc,
                                             uint32_t accumulate) {

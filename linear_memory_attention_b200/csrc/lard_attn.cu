@@ -269,10 +269,11 @@ Pass plan_simt(long long problems, long long R, int d, long long tiles) {
 // Tensor-core pass.  Up to 128 rows the two streams of a block share them and
 // take alternate key tiles; more rows take one tile of rows each.  The number
 // of splits is the one that a model of the pass's time gives, in cycles: a
-// step (two tiles' products and exponentials) takes about 2200, a block's
-// prologue and epilogue 6000, the join 8000 and its bytes; one step of a pass
-// that reads each key tile once cannot be faster than HBM (3400 B a cycle)
-// brings the tiles of all running blocks.
+// step (products and exponentials of two tiles) takes 3700, or as long as HBM
+// (3400 B a cycle) needs to bring the running blocks' tiles where each is read
+// once; a block's beginning and end 12000; partial rows are written, read and
+// joined at 3400 B a cycle by a kernel of its own, 8000.
+// (1 x 4096 rows of 32 heads over 16384 keys, 512 blocks: one split 1.10 ms, two 1.06 ms.)
 Pass plan_tc(long long problems, long long R, int d, long long tiles, long long rows) {
     Pass p;
     const bool by_keys = R <= 128;
@@ -282,11 +283,14 @@ Pass plan_tc(long long problems, long long R, int d, long long tiles, long long 
     double best = 0.0;
     const long long most = std::max(1LL, std::min(64LL, by_keys ? tiles / 2 : tiles));
     for (long long s = 1; s <= most; ++s) {
-        const long long waves = tiles_of(p.blocks * s, kSms), running = std::min<long long>(kSms, p.blocks * s);
+        const long long blocks = p.blocks * s, full = blocks / kSms, rest = blocks % kSms;
         const double steps = static_cast<double>(tiles_of(tiles_of(tiles, s), by_keys ? 2 : 1));
-        double step = 2200.0;
-        if (rtiles == 1) step = std::max(step, (by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
-        double cost = waves * (steps * step + 6000.0);
+        auto time = [&](long long running) {
+            double step = 3700.0;
+            if (rtiles == 1) step = std::max(step, (by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
+            return steps * step + 12000.0;
+        };
+        double cost = full * time(kSms) + (rest ? time(rest) : 0.0);
         if (s > 1) cost += 8000.0 + 8.0 * s * rows * d / 3400.0;
         if (s == 1 || cost < best) {
             best = cost;
