@@ -100,6 +100,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
     DqCtrl* ctrl = reinterpret_cast<DqCtrl*>(smem + L::OFF_CTRL);
     volatile int* abort_flag = &ctrl->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    next_may_start();
     const int R = g.G * g.n;
     const int rtiles = (R + 127) / 128;
     const int r0 = static_cast<int>(blockIdx.x % rtiles) * 128;
@@ -500,6 +501,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         for (int s = 0; s < L::NS && s < issued; ++s) drain(&ctrl->u_full[s], ((issued - 1 - s) / L::NS) & 1, dlim);
       } else if (warp == 2) {
         // ------------------------------------------------------------ row statistics of each unit
+        wait_for_kernel_before();  // delta
         for (int u = 0; u < U; ++u) {
             const int s = u % L::NS;
             const bool ok = ptx::mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,

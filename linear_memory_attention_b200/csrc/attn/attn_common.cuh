@@ -54,6 +54,7 @@ struct FwdArgs {
     // With join, the key tiles of a problem are dealt to `splits` blocks, each of
     // which leaves its rows' normalised O and LSE as partials split0 + split.
     int splits, split0, join;
+    int second;       // the call's second pass, which runs beside the first
     long long rows;   // B Hkv G n
     float* part_o;    // [partials][rows][D]
     float* part_lse;  // [partials][rows]

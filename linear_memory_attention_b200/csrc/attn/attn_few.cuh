@@ -38,6 +38,7 @@ struct FewArgs {
     int nseg, PB, Hkv, G, n, R;  // as in TcFwdArgs; R <= 16
     int cluster, splits;         // blocks of a cluster; clusters of a problem
     int split0, join;
+    int second;  // the call's second pass, which runs beside the first
     long long rows;
     float* part_o;
     float* part_lse;
@@ -84,6 +85,7 @@ struct FewLayout {
 template <int D>
 __global__ void __launch_bounds__(32 * kFewWarps, 3) attn_few_kernel(const __grid_constant__ FewArgs g) {
     using L = FewLayout<D>;
+    if (g.join) next_may_start();
     extern __shared__ uint8_t smem_raw[];
     uint8_t* few_smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     constexpr int KI = L::KI, NT = L::NT;
@@ -340,7 +342,8 @@ __global__ void __launch_bounds__(32 * kFewWarps, 3) attn_few_kernel(const __gri
             if (x == 0) g.lse[row] = lse;
         }
     }
-    if (g.cluster > 1) cluster.sync();  // no block leaves while another reads its rows
+    if (g.cluster > 1) cluster.sync();       // no block leaves while another reads its rows
+    if (g.second) wait_for_kernel_before();  // whoever waits for this pass has waited for the first
 }
 
 }  // namespace attn

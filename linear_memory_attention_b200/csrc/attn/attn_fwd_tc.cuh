@@ -55,6 +55,7 @@ struct TcFwdArgs {
     int nseg, PB, Hkv, G, n, R;
     int splits, split0;  // with join: partial rows go to split0 + split
     int join;
+    int second;  // the call's second pass, which runs beside the first
     long long rows;  // B Hkv G n
     float* part_o;
     float* part_lse;
@@ -101,6 +102,8 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     FwdTcCtrl* ctrl = reinterpret_cast<FwdTcCtrl*>(smem + L::OFF_CTRL);
     volatile int* abort_flag = &ctrl->abort_flag;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    if (g.join) next_may_start();
 
     constexpr int kRowsPerBlock = kByKeys ? 128 : 256;
     const int rtiles = (g.R + kRowsPerBlock - 1) / kRowsPerBlock;
@@ -502,6 +505,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     __syncthreads();
     ptx::tc_fence_after();
     if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    if (g.second) wait_for_kernel_before();  // whoever waits for this pass has waited for the first
 }
 
 }  // namespace attn

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "attn_common.cuh"
+#include "attn_ptx.cuh"
 
 namespace lard {
 namespace attn {
@@ -12,6 +13,7 @@ namespace attn {
 // One warp per row; lanes share the splits' weights, then the head dimension.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs<T> g) {
+    wait_for_kernel_before();
     const int lane = threadIdx.x & 31;
     const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (row >= g.rows) return;
@@ -70,6 +72,7 @@ struct SumArgs {
 // One warp per row; grid over the jobs' rows one after the other.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) attn_sum_kernel(const __grid_constant__ SumArgs<T> g) {
+    wait_for_kernel_before();
     const int lane = threadIdx.x & 31;
     long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     int k = 0;

@@ -7,6 +7,12 @@
 namespace lard {
 namespace attn {
 
+// Programmatic dependent launch: the next kernel of the call may start as soon
+// as every block of this one has begun (its blocks then fill SMs that this one
+// leaves idle); whoever reads what the kernel before wrote waits first.
+__device__ __forceinline__ void next_may_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_kernel_before() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 __device__ __forceinline__ void tma_load_4d(void* smem_dst, const CUtensorMap* map, uint64_t* bar, int x, int y, int z,
                                             int w) {
     asm volatile(

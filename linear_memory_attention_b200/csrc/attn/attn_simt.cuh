@@ -21,6 +21,7 @@
 
 #include "../lard_exp2.cuh"
 #include "attn_common.cuh"
+#include "attn_ptx.cuh"
 
 namespace lard {
 namespace attn {
@@ -140,6 +141,7 @@ __device__ __forceinline__ float4 scaled(float2 a, float2 b, float s) { return m
 template <int D, int RT>
 __global__ void __launch_bounds__(kSimtThreads) attn_fwd_simt_kernel(const __grid_constant__ FwdArgs<float> g) {
     using L = SimtLayout<D>;
+    if (g.join) next_may_start();
     constexpr int kRows = 8 * RT;
     extern __shared__ float4 smem4[];
     const int grp = threadIdx.x / kSimtGroup, me = threadIdx.x % kSimtGroup;
@@ -253,11 +255,10 @@ __global__ void __launch_bounds__(kSimtThreads) attn_fwd_simt_kernel(const __gri
         }
     }
     __syncthreads();
-    if (grp == 1) return;
 #pragma unroll
     for (int a = 0; a < RT; ++a) {
         const int t = RT * ty + a, r = r0 + t;
-        if (r >= g.R) continue;
+        if (grp == 1 || r >= g.R) continue;
         const float m1 = jm[2 * t], top = fmaxf(m[a], m1), base = top == -INFINITY ? 0.f : top;
         float w0 = exp2f(m[a] - base), w1 = exp2f(m1 - base);
         const float sum = l[a] * w0 + jm[2 * t + 1] * w1;
@@ -278,6 +279,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_fwd_simt_kernel(const __gri
             else g.lse[row] = lse;
         }
     }
+    if (g.second) wait_for_kernel_before();  // whoever waits for this pass has waited for the first
 }
 
 // Backward work of cross attention; rows and heads as in FwdArgs.
@@ -304,6 +306,7 @@ struct SimtBwdArgs {
 template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_dq_simt_kernel(const __grid_constant__ SimtBwdArgs g) {
     using L = SimtLayout<D>;
+    next_may_start();
     constexpr int RT = 8;
     extern __shared__ float4 smem4[];
     float* qs = reinterpret_cast<float*>(smem4);
@@ -432,6 +435,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_dq_simt_kernel(const __grid
 template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_dkdv_simt_kernel(const __grid_constant__ SimtBwdArgs g) {
     using L = SimtLayout<D>;
+    if (g.qsplits > 1 || g.ksplits > 1) next_may_start();
     constexpr int RT = 8;
     extern __shared__ float4 smem4[];
     float* ks = reinterpret_cast<float*>(smem4);
@@ -461,6 +465,7 @@ __global__ void __launch_bounds__(kSimtThreads) attn_dkdv_simt_kernel(const __gr
         simt_fetch<D, kSimtTile, kSimtThreads>(threadIdx.x, ks, len - j0, g.k.p, [&](int t) { return g.k.row(b, hk, j0 + t); });
         simt_fetch<D, kSimtTile, kSimtThreads>(threadIdx.x, vs, len - j0, g.v.p, [&](int t) { return g.v.row(b, hk, j0 + t); });
     }
+    wait_for_kernel_before();  // delta
     float2 acc[RT][D / 32];  // group 0: dV, group 1: dK
 #pragma unroll
     for (int a = 0; a < RT; ++a)

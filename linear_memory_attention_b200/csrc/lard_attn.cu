@@ -9,6 +9,7 @@
 #include <cstdint>
 #include <mutex>
 #include <type_traits>
+#include <utility>
 
 #include "lard_attn.h"
 #include "lard_host.h"
@@ -210,6 +211,34 @@ lard_status check_sizes(lard_dtype dtype, int B, int Hq, int Hkv, int n, int d, 
 template <typename T>
 View<T> view(const lard_attn_view& v) {
     return View<T>{static_cast<T*>(v.ptr), v.batch, v.head, v.row};
+}
+
+// Launches a kernel; `after`: it may start beside the kernel before it in the
+// call, and itself waits (attn_ptx.cuh) for what it reads of that one's.
+template <typename... Params, typename... Args>
+lard_status launch(void (*kernel)(Params...), long long grid, int threads, int smem, cudaStream_t stream, bool after,
+                   int cluster, Args&&... args) {
+    cudaLaunchConfig_t c = {};
+    c.gridDim = dim3(static_cast<unsigned>(grid));
+    c.blockDim = dim3(static_cast<unsigned>(threads));
+    c.dynamicSmemBytes = static_cast<size_t>(smem);
+    c.stream = stream;
+    cudaLaunchAttribute at[2];
+    if (cluster > 0) {
+        at[c.numAttrs].id = cudaLaunchAttributeClusterDimension;
+        at[c.numAttrs].val.clusterDim.x = static_cast<unsigned>(cluster);
+        at[c.numAttrs].val.clusterDim.y = at[c.numAttrs].val.clusterDim.z = 1;
+        ++c.numAttrs;
+    }
+    if (after) {
+        at[c.numAttrs].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        at[c.numAttrs].val.programmaticStreamSerializationAllowed = 1;
+        ++c.numAttrs;
+    }
+    c.attrs = at;
+    if (cudaLaunchKernelEx(&c, kernel, std::forward<Args>(args)...) == cudaSuccess) return LARD_OK;
+    cudaGetLastError();
+    return LARD_ERR_CUDA;
 }
 
 // ------------------------------------------------------------------ forward
@@ -437,6 +466,7 @@ void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, 
     a.R = static_cast<int>(f.group_rows() * (x.shared ? f.B : 1));
     a.splits = x.splits;
     a.split0 = split0;
+    a.second = split0 > 0;
     a.join = p.join();
     a.rows = p.rows;
     a.part_o = g.part_o;
@@ -452,12 +482,8 @@ lard_status run_simt(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, 
     pass_args(a, f, p, x, split0, g);
     a.seg[0] = g.seg[x.seg];
     a.seg[1] = g.seg[x.nseg > 1 ? x.seg + 1 : x.seg];
-    const unsigned grid = static_cast<unsigned>(x.blocks * x.splits);
-    if (x.kind == Pass::kSimtFew)
-        attn_fwd_simt_kernel<D, 2><<<grid, kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(a);
-    else
-        attn_fwd_simt_kernel<D, 8><<<grid, kSimtThreads, SimtLayout<D>::FWD_BYTES, stream>>>(a);
-    return LARD_OK;
+    return launch(x.kind == Pass::kSimtFew ? attn_fwd_simt_kernel<D, 2> : attn_fwd_simt_kernel<D, 8>, x.blocks * x.splits,
+                  kSimtThreads, SimtLayout<D>::FWD_BYTES, stream, a.second, 0, a);
 }
 
 // The key segments of a pass for TMA loads of box_rows rows.
@@ -490,18 +516,8 @@ lard_status run_few(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, c
     a.cluster = x.cluster;
     a.wait_ns = kWaitLimitNs;
     a.drain_ns = kDrainLimitNs;
-    cudaLaunchConfig_t c = {};
-    c.gridDim = dim3(static_cast<unsigned>(x.blocks * x.splits));
-    c.blockDim = dim3(32 * kFewWarps);
-    c.dynamicSmemBytes = FewLayout<D>::SMEM_BYTES;
-    c.stream = stream;
-    cudaLaunchAttribute at;
-    at.id = cudaLaunchAttributeClusterDimension;
-    at.val.clusterDim.x = static_cast<unsigned>(x.cluster);
-    at.val.clusterDim.y = at.val.clusterDim.z = 1;
-    c.attrs = &at;
-    c.numAttrs = 1;
-    return cudaLaunchKernelEx(&c, attn_few_kernel<D>, a) == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    return launch(attn_few_kernel<D>, x.blocks * x.splits, 32 * kFewWarps, FewLayout<D>::SMEM_BYTES, stream, a.second,
+                  x.cluster, a);
 }
 
 template <int D>
@@ -513,12 +529,8 @@ lard_status run_tc(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, co
     if (!make_segs(a.seg, f, x, 128)) return LARD_ERR_INVALID_ARG;
     a.wait_ns = kWaitLimitNs;
     a.drain_ns = kDrainLimitNs;
-    const unsigned grid = static_cast<unsigned>(x.blocks * x.splits);
-    if (x.kind == Pass::kTcKeys)
-        attn_fwd_tc_kernel<D, 1><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
-    else
-        attn_fwd_tc_kernel<D, 0><<<grid, kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream>>>(a);
-    return LARD_OK;
+    return launch(x.kind == Pass::kTcKeys ? attn_fwd_tc_kernel<D, 1> : attn_fwd_tc_kernel<D, 0>, x.blocks * x.splits,
+                  kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream, a.second, 0, a);
 }
 
 template <typename T, int D>
@@ -539,9 +551,7 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
         if (st != LARD_OK) return st;
         split0 += x.splits;
     }
-    if (p.join())
-        attn_join_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.rows, kJoinRowsPerBlock)), 256, 0, stream>>>(g);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    return p.join() ? launch(attn_join_kernel<T, D>, tiles_of(p.rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, g) : LARD_OK;
 }
 
 Fwd cross_work(const lard_cross_attn& a, const lard_attn_view* v = nullptr) {
@@ -694,17 +704,18 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_at
     g.tau = a.tau;
     g.wait_ns = kWaitLimitNs;
     g.drain_ns = kDrainLimitNs;
-    attn_dq_tc_kernel<D><<<static_cast<unsigned>(p.qblocks), kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream>>>(g);
-    attn_dkdv_tc_kernel<D><<<static_cast<unsigned>(p.kblocks), kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream>>>(g);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    const lard_status st = launch(attn_dq_tc_kernel<D>, p.qblocks, kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream, false, 0, g);
+    return st != LARD_OK
+               ? st
+               : launch(attn_dkdv_tc_kernel<D>, p.kblocks, kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream, true, 0, g);
 }
 
 // Adds the partial sums that a backward call left.
 template <typename T, int D>
-void run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
+lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
               const float* part_k, const float* part_v, cudaStream_t stream) {
     using namespace lard::attn;
-    if (p.sum_rows == 0) return;
+    if (p.sum_rows == 0) return LARD_OK;
     SumArgs<T> s;
     s.jobs = 0;
     if (p.qsplits > 1)
@@ -714,7 +725,7 @@ void run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (
         s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, keys, a.tau};
         s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, keys, 1.f};
     }
-    attn_sum_kernel<T, D><<<static_cast<unsigned>(tiles_of(p.sum_rows, kJoinRowsPerBlock)), 256, 0, stream>>>(s);
+    return launch(attn_sum_kernel<T, D>, tiles_of(p.sum_rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, s);
 }
 
 template <int D>
@@ -746,12 +757,11 @@ lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_
     g.ksplits = p.ksplits;
     g.cfac = log2_factor(a.tau);
     g.tau = a.tau;
-    attn_dq_simt_kernel<D>
-        <<<static_cast<unsigned>(p.qblocks * p.qsplits), kSimtThreads, SimtLayout<D>::DQ_BYTES, stream>>>(g);
-    attn_dkdv_simt_kernel<D>
-        <<<static_cast<unsigned>(p.kblocks * p.ksplits), kSimtThreads, SimtLayout<D>::DKDV_BYTES, stream>>>(g);
-    run_sums<float, D>(a, p, v, g.part_q, g.part_k, g.part_v, stream);
-    return cudaGetLastError() == cudaSuccess ? LARD_OK : LARD_ERR_CUDA;
+    lard_status st =
+        launch(attn_dq_simt_kernel<D>, p.qblocks * p.qsplits, kSimtThreads, SimtLayout<D>::DQ_BYTES, stream, false, 0, g);
+    if (st == LARD_OK)
+        st = launch(attn_dkdv_simt_kernel<D>, p.kblocks * p.ksplits, kSimtThreads, SimtLayout<D>::DKDV_BYTES, stream, true, 0, g);
+    return st == LARD_OK ? run_sums<float, D>(a, p, v, g.part_q, g.part_k, g.part_v, stream) : st;
 }
 
 lard_status launch_bwd(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
