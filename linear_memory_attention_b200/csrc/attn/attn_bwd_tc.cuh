@@ -52,15 +52,15 @@ struct TcBwdArgs {
 
 constexpr int kBwdTcThreads = 384;
 
-// Rounds 32 fp32 TMEM columns, times `scale`, to bf16 at dst.
-__device__ __forceinline__ void store_scaled32(__nv_bfloat16* dst, const float (&o)[32], float scale) {
-    uint4* p = reinterpret_cast<uint4*>(dst);
+// Rounds 32 fp32 columns, times `scale`, to bf16 into units first and up of a staged row of ROW bytes.
+template <int ROW>
+__device__ __forceinline__ void stage_bf16(uint32_t area, int lane, int first, const float (&o)[32], float scale) {
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        p[k] = make_uint4(ptx::pack_bf16x2(o[8 * k] * scale, o[8 * k + 1] * scale),
-                          ptx::pack_bf16x2(o[8 * k + 2] * scale, o[8 * k + 3] * scale),
-                          ptx::pack_bf16x2(o[8 * k + 4] * scale, o[8 * k + 5] * scale),
-                          ptx::pack_bf16x2(o[8 * k + 6] * scale, o[8 * k + 7] * scale));
+    for (int u = 0; u < 4; ++u)
+        ptx::st_shared_v4(stage_unit<ROW>(area, lane, first + u), ptx::pack_bf16x2(o[8 * u] * scale, o[8 * u + 1] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 2] * scale, o[8 * u + 3] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 4] * scale, o[8 * u + 5] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 6] * scale, o[8 * u + 7] * scale));
 }
 
 // ---------------------------------------------------------------------- dQ
@@ -68,17 +68,18 @@ template <int D>
 struct DqLayout {
     static constexpr int KC = D / 64;
     static constexpr int TILE = KC * 16384;
-    static constexpr int NS = 3;  // stages of the K ring and of the V ring
+    static constexpr int NK = 3, NV = 2;  // stages of the K and V rings
     static constexpr int OFF_DO = 0;
-    static constexpr int OFF_K = TILE;
-    static constexpr int OFF_V = OFF_K + NS * TILE;
-    static constexpr int OFF_CTRL = OFF_V + NS * TILE;
+    static constexpr int OFF_ROWS = TILE;  // Q on its way to TMEM, at the end dQ on its way out
+    static constexpr int OFF_K = 2 * TILE;
+    static constexpr int OFF_V = OFF_K + NK * TILE;
+    static constexpr int OFF_CTRL = OFF_V + NV * TILE;
     static constexpr int SMEM_BYTES = OFF_CTRL + 2048 + 1024;
     static_assert(SMEM_BYTES <= 232448, "too much shared memory");
 };
 
 struct DqCtrl {
-    uint64_t k_full[3], k_empty[3], v_full[3], v_empty[3];
+    uint64_t k_full[3], k_empty[3], v_full[2], v_empty[2], tail_ready;
     uint64_t ready, s_full, s_free, dz_full, dz_free, dq_full, mma_done;
     uint32_t tmem_base;
     int abort_flag;
@@ -110,12 +111,15 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
     const int T = (len + 127) / 128;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < L::NS; ++s) {
+        for (int s = 0; s < L::NK; ++s) {
             ptx::mbar_init(&ctrl->k_full[s], 1);
             ptx::mbar_init(&ctrl->k_empty[s], 1);
+        }
+        for (int s = 0; s < L::NV; ++s) {
             ptx::mbar_init(&ctrl->v_full[s], 1);
             ptx::mbar_init(&ctrl->v_empty[s], 1);
         }
+        ptx::mbar_init(&ctrl->tail_ready, 1);
         ptx::mbar_init(&ctrl->ready, 8);
         ptx::mbar_init(&ctrl->s_full, 1);
         ptx::mbar_init(&ctrl->s_free, 8);
@@ -146,113 +150,107 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
         // ------------------------------------------------------------ producer
         int nk = 0, nv = 0;
         for (int t = 0; t < T; ++t) {
-            const int s = t % L::NS;
-            const uint32_t parity = ((t / L::NS) & 1) ^ 1;
-            bool ok = ptx::mbar_wait(&ctrl->k_empty[s], parity, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
+            const int sk = t % L::NK, sv = t % L::NV;
+            bool ok = mbar_wait(&ctrl->k_empty[sk], ((t / L::NK) & 1) ^ 1, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(&ctrl->k_full[s], L::TILE);
+                ptx::mbar_arrive_expect_tx(&ctrl->k_full[sk], L::TILE);
                 for (int c = 0; c < L::KC; ++c)
-                    tma_load_4d(smem + L::OFF_K + s * L::TILE + c * 16384, &g.k, &ctrl->k_full[s], c * 64, t * 128,
+                    tma_load_4d(smem + L::OFF_K + sk * L::TILE + c * 16384, &g.k, &ctrl->k_full[sk], c * 64, t * 128,
                                 g.khead ? hk : 0, g.kbatch ? b : 0);
             }
             __syncwarp();
             ++nk;
-            ok = ptx::mbar_wait(&ctrl->v_empty[s], parity, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
+            ok = mbar_wait(&ctrl->v_empty[sv], ((t / L::NV) & 1) ^ 1, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
-                ptx::mbar_arrive_expect_tx(&ctrl->v_full[s], L::TILE);
+                ptx::mbar_arrive_expect_tx(&ctrl->v_full[sv], L::TILE);
                 for (int c = 0; c < L::KC; ++c)
-                    tma_load_4d(smem + L::OFF_V + s * L::TILE + c * 16384, &g.v, &ctrl->v_full[s], c * 64, t * 128,
+                    tma_load_4d(smem + L::OFF_V + sv * L::TILE + c * 16384, &g.v, &ctrl->v_full[sv], c * 64, t * 128,
                                 g.vhead ? hk : 0, g.vbatch ? b : 0);
             }
             __syncwarp();
             ++nv;
-        }
-        // Let every copy this warp started land before the block can exit.
-        for (int s = 0; s < L::NS; ++s) {
-            if (s < nk) drain(&ctrl->k_full[s], ((nk - 1 - s) / L::NS) & 1, dlim);
-            if (s < nv) drain(&ctrl->v_full[s], ((nv - 1 - s) / L::NS) & 1, dlim);
-        }
-      } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
-        constexpr uint32_t kIdescDq = ptx::idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kHi = ptx::sdesc_hi(1024);
-        const uint32_t do_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_DO), 16);
-        const uint32_t k_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16);
-        const uint32_t k_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16384);
-        const uint32_t v_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_V), 16);
-        constexpr uint32_t kStage = L::TILE >> 4;
-        auto issue_s = [&](int t) {  // S = Q K^T, dP = dO V^T of key tile t
-            const int s = t % L::NS;
-            bool ok = ptx::mbar_wait(&ctrl->k_full[s], (t / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-            if (!__all_sync(0xffffffffu, ok)) return false;
             if (t * 128 + 128 > len) {  // K rows past the end meet dZ = 0 in dQ: they must not be NaN
-                uint8_t* k = smem + L::OFF_K + s * L::TILE;
+                ok = mbar_wait(&ctrl->k_full[sk], (t / L::NK) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
+                if (!__all_sync(0xffffffffu, ok)) break;
+                uint8_t* k = smem + L::OFF_K + sk * L::TILE;
                 for (int e = (len - t * 128) * 8 + lane; e < 1024; e += 32)
                     for (int c = 0; c < L::KC; ++c)
                         *reinterpret_cast<uint4*>(k + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 ptx::fence_proxy_async_smem();
                 __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(&ctrl->tail_ready);
             }
-            if (lane == 0) {
-                const uint32_t kd = k_k + s * kStage;
+        }
+        // Let every copy this warp started land before the block can exit.
+        for (int s = 0; s < L::NK && s < nk; ++s) drain(&ctrl->k_full[s], ((nk - 1 - s) / L::NK) & 1, dlim);
+        for (int s = 0; s < L::NV && s < nv; ++s) drain(&ctrl->v_full[s], ((nv - 1 - s) / L::NV) & 1, dlim);
+      } else if (warp == 1) {
+        // ------------------------------------------------------------ MMA issuer (one thread)
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t kIdescDq = ptx::idesc_bf16(128, D, 0, 1);
+            constexpr uint32_t kHi = ptx::sdesc_hi(1024);
+            const uint32_t do_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_DO), 16);
+            const uint32_t k_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16);
+            const uint32_t k_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16384);
+            const uint32_t v_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_V), 16);
+            constexpr uint32_t kStage = L::TILE >> 4;
+            auto wait = [&](uint64_t* bar, int parity) {
+                return mbar_wait(bar, parity, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
+            };
+            int ks = 0, kp = 0, vs = 0, vp = 0;  // next stage of each ring and the parity of its round
+            auto issue_s = [&](bool tail) {      // S = Q K^T, dP = dO V^T of the next key tile
+                if (!wait(&ctrl->k_full[ks], kp) || (tail && !wait(&ctrl->tail_ready, 0))) return false;
+                const uint32_t kd = k_k + ks * kStage;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     if (kk == 0) ptx::umma_ts<0>(tmem + kDqTmemS, tmem + kDqTmemQ, kd, kHi, kIdescS);
                     else ptx::umma_ts<1>(tmem + kDqTmemS, tmem + kDqTmemQ + kk * 8, kd + ptx::desc_step_k(kk), kHi, kIdescS);
                 }
-            }
-            __syncwarp();
-            ok = ptx::mbar_wait(&ctrl->v_full[s], (t / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            if (lane == 0) {
-                const uint32_t vd = v_k + s * kStage;
+                if (!wait(&ctrl->v_full[vs], vp)) return false;
+                const uint32_t vd = v_k + vs * kStage;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     if (kk == 0) ptx::umma_ss<0>(tmem + kDqTmemDp, do_k, vd, kHi, kIdescS);
                     else ptx::umma_ss<1>(tmem + kDqTmemDp, do_k + ptx::desc_step_k(kk), vd + ptx::desc_step_k(kk), kHi, kIdescS);
                 }
-                ptx::umma_commit(&ctrl->v_empty[s]);
                 ptx::umma_commit(&ctrl->s_full);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = T > 0 && ptx::mbar_wait(&ctrl->ready, 0, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-        ok = __all_sync(0xffffffffu, ok);
-        if (ok) {
-            ptx::tc_fence_after();
-            ok = issue_s(0);
-        }
-        for (int t = 0; ok && t < T; ++t) {
-            if (t + 1 < T) {  // as soon as S and dP of tile t are in registers
-                ok = ptx::mbar_wait(&ctrl->s_free, t & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-                if (!(ok = __all_sync(0xffffffffu, ok))) break;
+                ptx::umma_commit(&ctrl->v_empty[vs]);
+                if (++ks == L::NK) { ks = 0; kp ^= 1; }
+                if (++vs == L::NV) { vs = 0; vp ^= 1; }
+                return true;
+            };
+            const bool ragged = len % 128 != 0;
+            bool ok = T > 0 && wait(&ctrl->ready, 0);
+            if (ok) {
                 ptx::tc_fence_after();
-                if (!(ok = issue_s(t + 1))) break;
+                ok = issue_s(ragged && T == 1);
             }
-            ok = ptx::mbar_wait(&ctrl->dz_full, t & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ptx::tc_fence_after();
-            if (lane == 0) {
-                const uint32_t kd = k_mn + (t % L::NS) * kStage;
+            int kq = 0;  // stage of the tile whose dZ comes next
+            for (int t = 0; ok && t < T; ++t) {
+                if (t + 1 < T) {  // as soon as S and dP of tile t are in registers
+                    if (!(ok = wait(&ctrl->s_free, t & 1))) break;
+                    ptx::tc_fence_after();
+                    if (!(ok = issue_s(ragged && t + 2 == T))) break;
+                }
+                if (!(ok = wait(&ctrl->dz_full, t & 1))) break;
+                ptx::tc_fence_after();
+                const uint32_t kd = k_mn + kq * kStage;
                 umma_ts_acc(tmem + kDqTmemDq, tmem + kDqTmemDz, kd, kHi, kIdescDq, t > 0 ? 1u : 0u);
 #pragma unroll
                 for (int kk = 1; kk < 8; ++kk)
                     ptx::umma_ts<1>(tmem + kDqTmemDq, tmem + kDqTmemDz + kk * 8, kd + ptx::desc_step_mn(kk), kHi, kIdescDq);
-                ptx::umma_commit(&ctrl->k_empty[t % L::NS]);
                 ptx::umma_commit(&ctrl->dz_free);
+                ptx::umma_commit(&ctrl->k_empty[kq]);
+                if (++kq == L::NK) kq = 0;
             }
-            __syncwarp();
-        }
-        if (lane == 0) {
             if (ok) ptx::umma_commit(&ctrl->dq_full);
             ptx::umma_commit(&ctrl->mma_done);
+            drain(&ctrl->mma_done, 0, dlim);
         }
         __syncwarp();
-        drain(&ctrl->mma_done, 0, dlim);
       }
     } else {
         ptx::regs_inc<kDqRegsSoft>();
@@ -265,60 +263,66 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
         const int head = hk * g.G + (row_ok ? r / g.n : 0), pos = row_ok ? r % g.n : 0;
         const size_t grow = static_cast<size_t>(bh) * R + (row_ok ? r : 0);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        // Prologue: Q rows into TMEM (half 0), dO rows into shared memory and delta (half 1).
-        if (half == 0) {
-            const uint4* src = reinterpret_cast<const uint4*>(g.q.row(b, head, pos));
+        // Prologue: Q and dO rows into shared memory, each warp half of its 32 rows;
+        // delta; Q on into TMEM.
+        const __nv_bfloat16* od = row_ok ? g.dout.row(b, head, pos) : nullptr;
+        {
+            const uint32_t q_area = ptx::smem_u32(smem + L::OFF_ROWS);
+            rows_to_operand<D>(q_area, q4 * 32, row_ok ? g.q.row(b, head, pos) : nullptr, lane, 16 * half, 16 * half + 16);
+            rows_to_operand<D>(ptx::smem_u32(smem + L::OFF_DO), q4 * 32, od, lane, 16 * half, 16 * half + 16);
+            copy_commit();
+            constexpr int kLanes = D / 8;
+            const __nv_bfloat16* oo = row_ok ? g.out.row(b, head, pos) : nullptr;
+#pragma unroll 4
+            for (int k = 16 * half; k < 16 * half + 16; k += 32 / kLanes) {
+                const int x = k + lane / kLanes, u = lane % kLanes;
+                const __nv_bfloat16 *pd = shfl_ptr(od, x), *po = shfl_ptr(oo, x);
+                float s = 0.f;
+                if (pd) {
+                    const uint4 d4 = __ldg(reinterpret_cast<const uint4*>(pd) + u), o4 = __ldg(reinterpret_cast<const uint4*>(po) + u);
+                    const uint32_t xs[4] = {d4.x, d4.y, d4.z, d4.w}, ys[4] = {o4.x, o4.y, o4.z, o4.w};
 #pragma unroll
-            for (int c = 0; c < D / 64; ++c) {
-                uint32_t w[32];
-#pragma unroll
-                for (int u = 0; u < 8; ++u) {
-                    uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                    if (row_ok) x = __ldg(src + c * 8 + u);
-                    w[4 * u] = x.x;
-                    w[4 * u + 1] = x.y;
-                    w[4 * u + 2] = x.z;
-                    w[4 * u + 3] = x.w;
+                    for (int e = 0; e < 4; ++e) {
+                        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
+                        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+                    }
                 }
-                __syncwarp();
-                ptx::tmem_st32(lane_base + kDqTmemQ + c * 32, w);
-            }
-            ptx::tmem_st_wait();
-            ptx::tc_fence_before();
-        } else {
-            const __nv_bfloat16* od = g.dout.row(b, head, pos);
-            const __nv_bfloat16* oo = g.out.row(b, head, pos);
-            const uint32_t dst = ptx::smem_u32(smem + L::OFF_DO) + row * 128;
-            float s = 0.f;
 #pragma unroll
-            for (int u = 0; u < D / 8; ++u) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u), y = x;
-                if (row_ok) {
-                    x = __ldg(reinterpret_cast<const uint4*>(od) + u);
-                    y = __ldg(reinterpret_cast<const uint4*>(oo) + u);
-                }
-                ptx::st_shared_v4(dst + (u >> 3) * 16384 + (((u & 7) ^ (row & 7)) << 4), x.x, x.y, x.z, x.w);
-                const uint32_t xs[4] = {x.x, x.y, x.z, x.w}, ys[4] = {y.x, y.y, y.z, y.w};
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    s = fmaf(__uint_as_float(xs[k] << 16), __uint_as_float(ys[k] << 16), s);
-                    s = fmaf(__uint_as_float(xs[k] & 0xffff0000u), __uint_as_float(ys[k] & 0xffff0000u), s);
+                for (int e = kLanes / 2; e > 0; e >>= 1) s += __shfl_xor_sync(0xffffffffu, s, e);
+                if (u == 0) {
+                    ctrl->delta[q4 * 32 + x] = s;
+                    if (pd) g.delta[static_cast<size_t>(bh) * R + r0 + q4 * 32 + x] = s;
                 }
             }
-            ctrl->delta[row] = s;
-            if (row_ok) g.delta[grow] = s;
+            copy_wait<0>();
             ptx::fence_proxy_async_smem();
+            ptx::named_bar_sync(1, 256);  // both halves of the rows are there
+            if (half == 0) {
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    uint32_t w[32];
+#pragma unroll
+                    for (int u = 0; u < 8; ++u)
+                        asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                                     : "=r"(w[4 * u]), "=r"(w[4 * u + 1]), "=r"(w[4 * u + 2]), "=r"(w[4 * u + 3])
+                                     : "r"(q_area + c * 16384 + row * 128 + ((u ^ (row & 7)) << 4))
+                                     : "memory");
+                    __syncwarp();
+                    ptx::tmem_st32(lane_base + kDqTmemQ + c * 32, w);
+                }
+                ptx::tmem_st_wait();
+                ptx::tc_fence_before();
+            }
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(&ctrl->ready);
         }
-        __syncwarp();
-        if (lane == 0) ptx::mbar_arrive(&ctrl->ready);
-        ptx::named_bar_sync(1, 256);
         const float delta = ctrl->delta[row];
         const float nl2 = row_ok ? -g.lse[grow] * kLog2e : 0.f;
         const float2 cf2 = splat2(g.cfac), nl22 = splat2(nl2), nd2 = splat2(-delta);
         bool ok = true;
         for (int t = 0; t < T; ++t) {
             const int seen = row_ok ? len - t * 128 - half * 64 : 0;  // of this thread's 64 keys
-            ok = ptx::mbar_wait(&ctrl->s_full, t & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
+            ok = mbar_wait(&ctrl->s_full, t & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             ptx::tc_fence_after();
             float z[2][32], dp[2][32];
@@ -347,7 +351,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
                 pk[k >> 1] = ptx::pack_bf16x2(x.x, x.y);
             }
             // dZ(t - 1) has been read by its product.
-            ok = ptx::mbar_wait(&ctrl->dz_free, (t & 1) ^ 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
+            ok = mbar_wait(&ctrl->dz_free, (t & 1) ^ 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             ptx::tc_fence_after();
             __syncwarp();
@@ -358,12 +362,12 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
             if (lane == 0) ptx::mbar_arrive(&ctrl->dz_full);
         }
         if (ok && T > 0) {
-            ok = ptx::mbar_wait(&ctrl->dq_full, 0, abort_flag, lim, &g_lard_fault, kFaultBwdEpilogue);
+            ok = mbar_wait(&ctrl->dq_full, 0, abort_flag, lim, &g_lard_fault, kFaultBwdEpilogue);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
         }
         if (ok) {
-            __nv_bfloat16* dst = g.dq.row(b, head, pos) + half * (D / 2);
+            const uint32_t area = ptx::smem_u32(smem + L::OFF_ROWS) + (half * 4 + q4) * (L::TILE / 8);
 #pragma unroll
             for (int c = 0; c < D / 2; c += 32) {
                 float o[32];
@@ -375,8 +379,9 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                if (row_ok) store_scaled32(dst + c, o, g.tau);
+                stage_bf16<D>(area, lane, c / 8, o, g.tau);
             }
+            staged_rows_out<D>(area, row_ok ? g.dq.row(b, head, pos) + half * (D / 2) : nullptr, lane);
         }
     }
     ptx::tc_fence_before();
@@ -481,7 +486,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         int issued = 0;
         for (int u = 0; u < U; ++u) {
             const int s = u % L::NS;
-            const bool ok = ptx::mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
+            const bool ok = mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
                                            kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         wait_for_kernel_before();  // delta
         for (int u = 0; u < U; ++u) {
             const int s = u % L::NS;
-            const bool ok = ptx::mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
+            const bool ok = mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
                                            kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
             const int i0 = u % upn * kUnit;
@@ -519,22 +524,24 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
             if (lane == 0) ptx::mbar_arrive(&ctrl->st_full[s]);
         }
       } else if (warp == 1) {
-        // ------------------------------------------------------------ MMA issuer
-        constexpr uint32_t kIdescS = ptx::idesc_bf16(128, kUnit, 0, 0);
-        constexpr uint32_t kIdescAcc = ptx::idesc_bf16(128, D, 0, 1);
-        constexpr uint32_t kHi = ptx::sdesc_hi(1024);
-        const uint32_t k_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16);
-        const uint32_t v_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_V), 16);
-        const uint32_t u_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_U), 16);
-        const uint32_t u_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_U), 8192);
-        constexpr uint32_t kQ = 2 * L::UNIT >> 4, kDo = L::UNIT >> 4;
-        auto issue_s = [&](int u) {  // S^T = K Q^T, dP^T = V dO^T of unit u
-            const int s = u % L::NS;
-            const bool ok = ptx::mbar_wait(&ctrl->u_full[s], (u / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-            if (!__all_sync(0xffffffffu, ok)) return false;
-            if (lane == 0) {
-                const uint32_t q = u_k + s * kQ, o = q + kDo;
-                const uint32_t ts = tmem + 256 + (u & 1) * 64, tp = ts + 128;
+        // ------------------------------------------------------------ MMA issuer (one thread)
+        if (lane == 0) {
+            constexpr uint32_t kIdescS = ptx::idesc_bf16(128, kUnit, 0, 0);
+            constexpr uint32_t kIdescAcc = ptx::idesc_bf16(128, D, 0, 1);
+            constexpr uint32_t kHi = ptx::sdesc_hi(1024);
+            const uint32_t k_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_K), 16);
+            const uint32_t v_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_V), 16);
+            const uint32_t u_k = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_U), 16);
+            const uint32_t u_mn = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_U), 8192);
+            constexpr uint32_t kQ = 2 * L::UNIT >> 4, kDo = L::UNIT >> 4;
+            auto wait = [&](uint64_t* bar, int parity) {
+                return mbar_wait(bar, parity, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
+            };
+            int next = 0, np = 0;             // stage of the next unit and the parity of its round
+            auto issue_s = [&](int stream) {  // S^T = K Q^T, dP^T = V dO^T of the next unit
+                if (!wait(&ctrl->u_full[next], np)) return false;
+                const uint32_t q = u_k + next * kQ, o = q + kDo;
+                const uint32_t ts = tmem + 256 + stream * 64, tp = ts + 128;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     if (kk == 0) ptx::umma_ss<0>(ts, k_k, q, kHi, kIdescS);
@@ -545,22 +552,19 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
                     if (kk == 0) ptx::umma_ss<0>(tp, v_k, o, kHi, kIdescS);
                     else ptx::umma_ss<1>(tp, v_k + ptx::desc_step_k(kk), o + desc_step_k64(kk), kHi, kIdescS);
                 }
-                ptx::umma_commit(&ctrl->s_full[u & 1]);
-            }
-            __syncwarp();
-            return true;
-        };
-        bool ok = U > 0 && ptx::mbar_wait(&ctrl->kv_full, 0, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-        ok = __all_sync(0xffffffffu, ok);
-        for (int u = 0; ok && u < 2 && u < U; ++u) ok = issue_s(u);
-        for (int u = 0; ok && u < U; ++u) {
-            const int s = u % L::NS;
-            ok = ptx::mbar_wait(&ctrl->p_full[u & 1], (u >> 1) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdMma);
-            if (!(ok = __all_sync(0xffffffffu, ok))) break;
-            ptx::tc_fence_after();
-            if (lane == 0) {
+                ptx::umma_commit(&ctrl->s_full[stream]);
+                if (++next == L::NS) { next = 0; np ^= 1; }
+                return true;
+            };
+            bool ok = U > 0 && wait(&ctrl->kv_full, 0);
+            for (int u = 0; ok && u < 2 && u < U; ++u) ok = issue_s(u);
+            int s = 0;
+            for (int u = 0; ok && u < U; ++u) {
+                const int stream = u & 1;
+                if (!(ok = wait(&ctrl->p_full[stream], (u >> 1) & 1))) break;
+                ptx::tc_fence_after();
                 const uint32_t q = u_mn + s * kQ, o = q + kDo;
-                const uint32_t tp = tmem + 256 + (u & 1) * 64, tz = tp + 128;
+                const uint32_t tp = tmem + 256 + stream * 64, tz = tp + 128;
                 umma_ts_acc(tmem, tp, o, kHi, kIdescAcc, u > 0 ? 1u : 0u);
 #pragma unroll
                 for (int kk = 1; kk < kUnit / 16; ++kk) ptx::umma_ts<1>(tmem, tp + kk * 8, o + ptx::desc_step_mn(kk), kHi, kIdescAcc);
@@ -569,16 +573,14 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
                 for (int kk = 1; kk < kUnit / 16; ++kk)
                     ptx::umma_ts<1>(tmem + 128, tz + kk * 8, q + ptx::desc_step_mn(kk), kHi, kIdescAcc);
                 ptx::umma_commit(&ctrl->u_empty[s]);
+                if (++s == L::NS) s = 0;
+                if (u + 2 < U) ok = issue_s(stream);  // behind the products that read P^T and dZ^T in its place
             }
-            __syncwarp();
-            if (u + 2 < U) ok = issue_s(u + 2);  // behind the products that read P^T and dZ^T in its place
-        }
-        if (lane == 0) {
             if (ok) ptx::umma_commit(&ctrl->acc_full);
             ptx::umma_commit(&ctrl->mma_done);
+            drain(&ctrl->mma_done, 0, dlim);
         }
         __syncwarp();
-        drain(&ctrl->mma_done, 0, dlim);
       }
     } else {
         ptx::regs_inc<kDqRegsSoft>();
@@ -592,8 +594,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         bool ok = true;
         for (int u = i; u < U; u += 2) {
             const int s = u % L::NS;
-            ok = ptx::mbar_wait(&ctrl->st_full[s], (u / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax) &&
-                 ptx::mbar_wait(&ctrl->s_full[i], (u >> 1) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
+            ok = mbar_wait(&ctrl->st_full[s], (u / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax) &&
+                 mbar_wait(&ctrl->s_full[i], (u >> 1) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             ptx::tc_fence_after();
             float z[2][32], dp[2][32];
@@ -633,12 +635,13 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
             if (lane == 0) ptx::mbar_arrive(&ctrl->p_full[i]);
         }
         if (ok && U > 0) {
-            ok = ptx::mbar_wait(&ctrl->acc_full, 0, abort_flag, lim, &g_lard_fault, kFaultBwdEpilogue);
+            ok = mbar_wait(&ctrl->acc_full, 0, abort_flag, lim, &g_lard_fault, kFaultBwdEpilogue);
             ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
         }
         if (ok) {  // warpgroup 0 writes dV, 1 dK; keys past the length get zeros
-            __nv_bfloat16* dst = (i ? g.dk : g.dv).row(b, hk, key < g.m ? key : 0);
+            // Through K's tile and V's, which the last S^T and dP^T have read.
+            const uint32_t area = ptx::smem_u32(smem + (i ? L::OFF_K : L::OFF_V)) + q4 * (L::TILE / 4);
             const float scale = i ? g.tau : 1.f;
 #pragma unroll
             for (int c = 0; c < D; c += 32) {
@@ -652,8 +655,9 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                if (key < g.m) store_scaled32(dst + c, o, scale);
+                stage_bf16<D * 2>(area, lane, c / 8, o, scale);
             }
+            staged_rows_out<D * 2>(area, key < g.m ? (i ? g.dk : g.dv).row(b, hk, key) : nullptr, lane);
         }
     }
     ptx::tc_fence_before();
