@@ -40,6 +40,10 @@ struct TcBwdArgs {
     float* delta;
     const int* len;
     int m, B, Hkv, G, n;
+    // More than one split: sums go to [split][row][D] buffers, rows of dq in the
+    // order (b, head, i), of dk and dv in the order (b, key head, j).
+    int qsplits, ksplits;
+    float *part_q, *part_k, *part_v;
     int khead, kbatch, vhead, vbatch, qhead, qbatch, dohead, dobatch;  // 0 where one block is shared
     float cfac, tau;
     unsigned long long wait_ns, drain_ns;
@@ -61,6 +65,20 @@ __device__ __forceinline__ void stage_bf16(uint32_t area, int lane, int first, c
                           ptx::pack_bf16x2(o[8 * u + 2] * scale, o[8 * u + 3] * scale),
                           ptx::pack_bf16x2(o[8 * u + 4] * scale, o[8 * u + 5] * scale),
                           ptx::pack_bf16x2(o[8 * u + 6] * scale, o[8 * u + 7] * scale));
+}
+
+// Writes 32 fp32 columns of a warp's 32 rows, COLS at a time through the area.
+template <int COLS>
+__device__ __forceinline__ void fp32_rows_out(uint32_t area, int lane, const float (&o)[32], float* mine) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
+#pragma unroll
+    for (int x = 0; x < 32; x += COLS) {
+#pragma unroll
+        for (int u = 0; u < COLS / 4; ++u)
+            ptx::st_shared_v4(stage_unit<COLS * 4>(area, lane, u), w[x + 4 * u], w[x + 4 * u + 1], w[x + 4 * u + 2],
+                              w[x + 4 * u + 3]);
+        staged_rows_out<COLS * 4>(area, mine ? mine + x : nullptr, lane);
+    }
 }
 
 // ---------------------------------------------------------------------- dQ
@@ -92,7 +110,7 @@ constexpr int kDqRegsLaunch = 168, kDqRegsCtl = 80, kDqRegsSoft = 208;
 constexpr int kDqRegsSplitTotal = 128 * (kDqRegsCtl + 2 * kDqRegsSoft);
 static_assert(kDqRegsSplitTotal <= kBwdTcThreads * kDqRegsLaunch, "register split exceeds the launch allocation");
 
-// Grid: row tiles (fastest), then B * Hkv.
+// Grid: row tiles (fastest), splits of the keys, B * Hkv.
 template <int D>
 __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __grid_constant__ TcBwdArgs g) {
     using L = DqLayout<D>;
@@ -105,10 +123,14 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
     const int R = g.G * g.n;
     const int rtiles = (R + 127) / 128;
     const int r0 = static_cast<int>(blockIdx.x % rtiles) * 128;
-    const int bh = static_cast<int>(blockIdx.x / rtiles);
+    const int split = static_cast<int>(blockIdx.x / rtiles % g.qsplits);
+    const int bh = static_cast<int>(blockIdx.x / rtiles / g.qsplits);
     const int b = bh / g.Hkv, hk = bh % g.Hkv;
     const int len = g.length(b);
-    const int T = (len + 127) / 128;
+    // This block's key tiles [t0, t0 + T).
+    const int tiles = (len + 127) / 128;
+    const int t0 = static_cast<int>(static_cast<long long>(tiles) * split / g.qsplits);
+    const int T = static_cast<int>(static_cast<long long>(tiles) * (split + 1) / g.qsplits) - t0;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::NK; ++s) {
@@ -156,7 +178,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(&ctrl->k_full[sk], L::TILE);
                 for (int c = 0; c < L::KC; ++c)
-                    tma_load_4d(smem + L::OFF_K + sk * L::TILE + c * 16384, &g.k, &ctrl->k_full[sk], c * 64, t * 128,
+                    tma_load_4d(smem + L::OFF_K + sk * L::TILE + c * 16384, &g.k, &ctrl->k_full[sk], c * 64, (t0 + t) * 128,
                                 g.khead ? hk : 0, g.kbatch ? b : 0);
             }
             __syncwarp();
@@ -166,16 +188,16 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
             if (lane == 0) {
                 ptx::mbar_arrive_expect_tx(&ctrl->v_full[sv], L::TILE);
                 for (int c = 0; c < L::KC; ++c)
-                    tma_load_4d(smem + L::OFF_V + sv * L::TILE + c * 16384, &g.v, &ctrl->v_full[sv], c * 64, t * 128,
+                    tma_load_4d(smem + L::OFF_V + sv * L::TILE + c * 16384, &g.v, &ctrl->v_full[sv], c * 64, (t0 + t) * 128,
                                 g.vhead ? hk : 0, g.vbatch ? b : 0);
             }
             __syncwarp();
             ++nv;
-            if (t * 128 + 128 > len) {  // K rows past the end meet dZ = 0 in dQ: they must not be NaN
+            if ((t0 + t) * 128 + 128 > len) {  // K rows past the end meet dZ = 0 in dQ: they must not be NaN
                 ok = mbar_wait(&ctrl->k_full[sk], (t / L::NK) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdProducer);
                 if (!__all_sync(0xffffffffu, ok)) break;
                 uint8_t* k = smem + L::OFF_K + sk * L::TILE;
-                for (int e = (len - t * 128) * 8 + lane; e < 1024; e += 32)
+                for (int e = (len - (t0 + t) * 128) * 8 + lane; e < 1024; e += 32)
                     for (int c = 0; c < L::KC; ++c)
                         *reinterpret_cast<uint4*>(k + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                 ptx::fence_proxy_async_smem();
@@ -222,7 +244,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
                 if (++vs == L::NV) { vs = 0; vp ^= 1; }
                 return true;
             };
-            const bool ragged = len % 128 != 0;
+            const bool ragged = len % 128 != 0 && t0 + T == tiles;  // the last of these tiles is
             bool ok = T > 0 && wait(&ctrl->ready, 0);
             if (ok) {
                 ptx::tc_fence_after();
@@ -291,7 +313,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
                 for (int e = kLanes / 2; e > 0; e >>= 1) s += __shfl_xor_sync(0xffffffffu, s, e);
                 if (u == 0) {
                     ctrl->delta[q4 * 32 + x] = s;
-                    if (pd) g.delta[static_cast<size_t>(bh) * R + r0 + q4 * 32 + x] = s;
+                    if (pd && split == 0) g.delta[static_cast<size_t>(bh) * R + r0 + q4 * 32 + x] = s;
                 }
             }
             copy_wait<0>();
@@ -321,7 +343,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
         const float2 cf2 = splat2(g.cfac), nl22 = splat2(nl2), nd2 = splat2(-delta);
         bool ok = true;
         for (int t = 0; t < T; ++t) {
-            const int seen = row_ok ? len - t * 128 - half * 64 : 0;  // of this thread's 64 keys
+            const int seen = row_ok ? len - (t0 + t) * 128 - half * 64 : 0;  // of this thread's 64 keys
             ok = mbar_wait(&ctrl->s_full, t & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax);
             if (!(ok = __all_sync(0xffffffffu, ok))) break;
             ptx::tc_fence_after();
@@ -379,9 +401,16 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                stage_bf16<D>(area, lane, c / 8, o, g.tau);
+                if (g.qsplits > 1)
+                    fp32_rows_out<D / 4>(area, lane, o,
+                                         row_ok ? g.part_q + (static_cast<size_t>(split) * g.B * g.Hkv * R + grow) * D +
+                                                      half * (D / 2) + c
+                                                : nullptr);
+                else
+                    stage_bf16<D>(area, lane, c / 8, o, g.tau);
             }
-            staged_rows_out<D>(area, row_ok ? g.dq.row(b, head, pos) + half * (D / 2) : nullptr, lane);
+            if (g.qsplits == 1)
+                staged_rows_out<D>(area, row_ok ? g.dq.row(b, head, pos) + half * (D / 2) : nullptr, lane);
         }
     }
     ptx::tc_fence_before();
@@ -422,7 +451,7 @@ static_assert(sizeof(DkvCtrl) <= 4096, "control block too large");
 // Descriptor low-word step for K step kk of a 64-row, K-major unit (8 KB a 64-column chunk).
 __host__ __device__ constexpr uint32_t desc_step_k64(int kk) { return (kk >> 2) * (8192 >> 4) + (kk & 3) * (32 >> 4); }
 
-// Grid: key tiles of m (fastest), then B * Hkv.
+// Grid: key tiles of m (fastest), splits of the rows, B * Hkv.
 template <int D>
 __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __grid_constant__ TcBwdArgs g) {
     using L = DkvLayout<D>;
@@ -433,11 +462,16 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int ktiles = (g.m + 127) / 128;
     const int j0 = static_cast<int>(blockIdx.x % ktiles) * 128;
-    const int bh = static_cast<int>(blockIdx.x / ktiles);
+    const int split = static_cast<int>(blockIdx.x / ktiles % g.ksplits);
+    const int bh = static_cast<int>(blockIdx.x / ktiles / g.ksplits);
     const int b = bh / g.Hkv, hk = bh % g.Hkv;
     const int len = g.length(b);
+    // This block's units [u0, u0 + U), those of the group's heads in a row.
     const int upn = (g.n + kUnit - 1) / kUnit;  // units of a head
-    const int U = j0 < len ? g.G * upn : 0;
+    const int units = j0 < len ? g.G * upn : 0;
+    const int u0 = static_cast<int>(static_cast<long long>(units) * split / g.ksplits);
+    const int U = static_cast<int>(static_cast<long long>(units) * (split + 1) / g.ksplits) - u0;
+    if (g.qsplits > 1 || g.ksplits > 1) next_may_start();
 
     if (threadIdx.x == 0) {
         ptx::mbar_init(&ctrl->kv_full, 1);
@@ -490,7 +524,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
                                            kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
             if (lane == 0) {
-                const int head = hk * g.G + u / upn, i0 = u % upn * kUnit;
+                const int head = hk * g.G + (u0 + u) / upn, i0 = (u0 + u) % upn * kUnit;
                 uint8_t* dst = smem + L::OFF_U + s * 2 * L::UNIT;
                 ptx::mbar_arrive_expect_tx(&ctrl->u_full[s], 2 * L::UNIT);
                 for (int c = 0; c < L::KC; ++c) {
@@ -512,8 +546,8 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
             const bool ok = mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
                                            kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
-            const int i0 = u % upn * kUnit;
-            const size_t at = (static_cast<size_t>(bh) * g.G + u / upn) * g.n + i0;
+            const int i0 = (u0 + u) % upn * kUnit;
+            const size_t at = (static_cast<size_t>(bh) * g.G + (u0 + u) / upn) * g.n + i0;
 #pragma unroll
             for (int k = 0; k < kUnit; k += 32) {
                 const bool in = i0 + k + lane < g.n;
@@ -655,9 +689,15 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                stage_bf16<D * 2>(area, lane, c / 8, o, scale);
+                if (g.ksplits > 1)
+                    fp32_rows_out<32>(area, lane, o,
+                                      key < g.m ? (i ? g.part_k : g.part_v) +
+                                                      ((static_cast<size_t>(split) * g.B * g.Hkv + bh) * g.m + key) * D + c
+                                                : nullptr);
+                else
+                    stage_bf16<D * 2>(area, lane, c / 8, o, scale);
             }
-            staged_rows_out<D * 2>(area, key < g.m ? (i ? g.dk : g.dv).row(b, hk, key) : nullptr, lane);
+            if (g.ksplits == 1) staged_rows_out<D * 2>(area, key < g.m ? (i ? g.dk : g.dv).row(b, hk, key) : nullptr, lane);
         }
     }
     ptx::tc_fence_before();

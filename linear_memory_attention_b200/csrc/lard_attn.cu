@@ -655,10 +655,9 @@ BwdPlan plan_bwd(const lard_cross_attn& a) {
     const int tile = a.dtype == LARD_DTYPE_FP32 ? lard::attn::kSimtTile : 128;
     p.qblocks = BH * tiles_of(R, tile);
     p.kblocks = BH * tiles_of(a.m, tile);
-    if (a.dtype == LARD_DTYPE_FP32) {
-        p.qsplits = split_to_fill(p.qblocks, tiles_of(a.m, tile), simt_slots(a.d));
-        p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), simt_slots(a.d));
-    }
+    const int slots = a.dtype == LARD_DTYPE_FP32 ? simt_slots(a.d) : kSms;
+    p.qsplits = split_to_fill(p.qblocks, tiles_of(a.m, tile), slots);
+    p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), slots);
     if (p.qsplits > 1) {
         p.part_q = static_cast<size_t>(p.qsplits) * BH * R * a.d * 4;
         p.sum_rows += BH * R;
@@ -668,6 +667,35 @@ BwdPlan plan_bwd(const lard_cross_attn& a) {
         p.sum_rows += 2 * BH * a.m;
     }
     return p;
+}
+
+// delta and the partial sums' places in the workspace.
+template <typename Args>
+void take_bwd_workspace(Args& g, const BwdPlan& p, void* ws) {
+    char* w = static_cast<char*>(ws);
+    g.delta = reinterpret_cast<float*>(w);
+    g.part_q = reinterpret_cast<float*>(w + p.delta);
+    g.part_k = reinterpret_cast<float*>(w + p.delta + p.part_q);
+    g.part_v = reinterpret_cast<float*>(w + p.delta + p.part_q + p.part_kv);
+    g.qsplits = p.qsplits;
+    g.ksplits = p.ksplits;
+}
+
+// Adds the partial sums that a backward call left.
+template <typename T, int D>
+lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
+              const float* part_k, const float* part_v, cudaStream_t stream) {
+    using namespace lard::attn;
+    if (p.sum_rows == 0) return LARD_OK;
+    SumArgs<T> s;
+    s.jobs = 0;
+    if (p.qsplits > 1)
+        s.job[s.jobs++] = {part_q, view<T>(v[5]), p.qsplits, a.Hq, a.n, static_cast<long long>(a.B) * a.Hq * a.n, a.tau};
+    if (p.ksplits > 1) {
+        s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, static_cast<long long>(a.B) * a.Hkv * a.m, a.tau};
+        s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, static_cast<long long>(a.B) * a.Hkv * a.m, 1.f};
+    }
+    return launch(attn_sum_kernel<T, D>, tiles_of(p.sum_rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, s);
 }
 
 template <int D>
@@ -685,7 +713,7 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_at
     g.dk = view<bf16>(v[6]);
     g.dv = view<bf16>(v[7]);
     g.lse = a.lse;
-    g.delta = static_cast<float*>(ws);
+    take_bwd_workspace(g, p, ws);
     g.len = a.k_len;
     g.m = a.m;
     g.B = a.B;
@@ -704,28 +732,11 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_at
     g.tau = a.tau;
     g.wait_ns = kWaitLimitNs;
     g.drain_ns = kDrainLimitNs;
-    const lard_status st = launch(attn_dq_tc_kernel<D>, p.qblocks, kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream, false, 0, g);
-    return st != LARD_OK
-               ? st
-               : launch(attn_dkdv_tc_kernel<D>, p.kblocks, kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream, true, 0, g);
-}
-
-// Adds the partial sums that a backward call left.
-template <typename T, int D>
-lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
-              const float* part_k, const float* part_v, cudaStream_t stream) {
-    using namespace lard::attn;
-    if (p.sum_rows == 0) return LARD_OK;
-    SumArgs<T> s;
-    s.jobs = 0;
-    if (p.qsplits > 1)
-        s.job[s.jobs++] = {part_q, view<T>(v[5]), p.qsplits, a.Hq, a.n, static_cast<long long>(a.B) * a.Hq * a.n, a.tau};
-    if (p.ksplits > 1) {
-        const long long keys = static_cast<long long>(a.B) * a.Hkv * a.m;
-        s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, keys, a.tau};
-        s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, keys, 1.f};
-    }
-    return launch(attn_sum_kernel<T, D>, tiles_of(p.sum_rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, s);
+    lard_status st =
+        launch(attn_dq_tc_kernel<D>, p.qblocks * p.qsplits, kBwdTcThreads, DqLayout<D>::SMEM_BYTES, stream, false, 0, g);
+    if (st == LARD_OK)
+        st = launch(attn_dkdv_tc_kernel<D>, p.kblocks * p.ksplits, kBwdTcThreads, DkvLayout<D>::SMEM_BYTES, stream, true, 0, g);
+    return st == LARD_OK ? run_sums<bf16, D>(a, p, v, g.part_q, g.part_k, g.part_v, stream) : st;
 }
 
 template <int D>
@@ -742,19 +753,13 @@ lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_
     g.dk = view<float>(v[6]);
     g.dv = view<float>(v[7]);
     g.lse = a.lse;
-    char* w = static_cast<char*>(ws);
-    g.delta = reinterpret_cast<float*>(w);
-    g.part_q = reinterpret_cast<float*>(w + p.delta);
-    g.part_k = reinterpret_cast<float*>(w + p.delta + p.part_q);
-    g.part_v = reinterpret_cast<float*>(w + p.delta + p.part_q + p.part_kv);
+    take_bwd_workspace(g, p, ws);
     g.len = a.k_len;
     g.m = a.m;
     g.B = a.B;
     g.Hkv = a.Hkv;
     g.G = a.Hq / a.Hkv;
     g.n = a.n;
-    g.qsplits = p.qsplits;
-    g.ksplits = p.ksplits;
     g.cfac = log2_factor(a.tau);
     g.tau = a.tau;
     lard_status st =

@@ -119,6 +119,19 @@ def test_few_rows_over_many_keys(att, n, m, dtype):
     au.check(att.cross_attention(q, k, v, tau, lens(k_len)), au.cross(q, k, v, tau, k_len))
 
 
+@pytest.mark.parametrize("n,m", [(3, 3000), (700, 40), (130, 400), (1, 257)])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+def test_gradients_of_long_and_narrow_calls(att, n, m, dtype, d):
+    """Few blocks along one axis: the other is split and its partial sums are added; some
+    splits have nothing to do."""
+    q, k, v, do, tau = cross_inputs(2, 4, 2, n, m, d, dtype, seed=35)
+    k_len = [m, 30]
+    got = att.cross_attention(q, k, v, tau, lens(k_len), dout=do)
+    att.lard_attn_device_status()
+    au.check(got, au.cross(q, k, v, tau, k_len, do))
+
+
 def test_large_and_rising_logits(att):
     """Row maxima that rise tile after tile by far, and logits of several hundreds."""
     for dtype in (BF16, FP32):
