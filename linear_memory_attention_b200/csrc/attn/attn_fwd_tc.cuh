@@ -1,11 +1,12 @@
 // attn_fwd_tc.cuh -- the forward pass on the 5th-generation tensor cores (bf16).
 //
-// A block works on two streams at a time, so that the tensor pipe has one
-// stream's products while the other's exponentials are computed.  By rows
-// (kByKeys = 0): stream i owns the 128 query rows of its own tile, and both
-// read every key tile.  By keys (kByKeys = 1; at most 128 rows): both streams
-// own the same rows, stream i the key tiles 2t + i, and the two are joined at
-// the end.  Per stream and key tile of 128:
+// A stream owns 128 query rows and a run of key tiles; a block works on two, so
+// that the tensor pipe has one stream's products while the other's exponentials
+// are computed.  By rows (kByKeys = 0): stream i owns the rows of its own tile,
+// and both read every key tile.  By keys (kByKeys = 1; at most 128 rows): both own the
+// same rows, stream i the key tiles 2t + i, and the two are joined at the end.
+// Per stream and key tile of KT (128; 64 at d = 64, where tensor memory then has room for two
+// blocks an SM, and exponentials, not products, are the bound):
 //   S = Q K^T      A = Q (shared memory, K-major), B = K (K-major)
 //   P = 2^(S c - m), row sums in fp32, P rounded to bf16 over S's TMEM columns
 //   O += P V       A = P (TMEM), B = V (MN-major), O in TMEM
@@ -18,11 +19,11 @@
 // Key tiles past a sequence's length are never visited.  Values of rows past
 // it inside the last tile are zeroed in shared memory before the product (0
 // times what is there could be NaN); their logits are replaced by -infinity.
-// TMEM (512 columns): S0 [0, 128), S1 [128, 256), O0 [256, 256 + D), O1 [384, 384 + D).
-// Roles (384 threads):
+// TMEM: S of stream i at 128 i, O behind the streams' S.
+// Roles:
 //   warp 0       TMA producer of the K / V ring
 //   warp 1       TMEM owner, MMA issuer
-//   warps 4-11   one stream each warpgroup: Q rows into shared memory, softmax
+//   warps 4 on   a warpgroup for each stream: Q rows into shared memory, softmax
 //                (one row a thread), the epilogue
 #pragma once
 
@@ -63,22 +64,33 @@ struct TcFwdArgs {
     unsigned long long wait_ns, drain_ns;
 };
 
-template <int D>
+template <int D, int kByKeys>
 struct FwdTcLayout {
+    static constexpr int KT = D == 64 ? 64 : 128;  // keys of a tile
     static constexpr int KC = D / 64;
-    static constexpr int TILE = KC * 16384;
-    static constexpr int NS = D == 128 ? 5 : 10;
+    static constexpr int TILE = KC * 16384;     // 128 rows of Q
+    static constexpr int KV_TILE = KC * KT * 128;  // a K or V tile
+    static constexpr int BLOCKS_PER_SM = D == 64 ? 2 : 1;
+    static constexpr int NS = D == 64 ? 8 : (kByKeys ? 6 : 5);
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_KV = 2 * TILE;
-    static constexpr int OFF_CTRL = OFF_KV + NS * TILE;
+    static constexpr int OFF_KV = (kByKeys ? 1 : 2) * TILE;
+    static constexpr int OFF_CTRL = OFF_KV + NS * KV_TILE;
     static constexpr int SMEM_BYTES = OFF_CTRL + 2048 + 1024;
     // By keys, the join stages a stream's O in the ring: 128 x D fp32.
-    static_assert(NS * TILE >= 128 * D * 4, "no room for the join");
-    static_assert(SMEM_BYTES <= 232448, "too much shared memory");
+    static_assert(!kByKeys || NS * KV_TILE >= 128 * D * 4, "no room for the join");
+    static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "too much shared memory");
+    // Tensor memory: S of stream i at KT i, O at TMEM_O + TMEM_O_STEP i.
+    static constexpr int TMEM_COLS = 512 / BLOCKS_PER_SM, TMEM_O = TMEM_COLS / 2, TMEM_O_STEP = TMEM_COLS / 4;
+    static_assert(2 * KT <= TMEM_O && D <= TMEM_O_STEP, "too much tensor memory");
+    // Registers a thread, and how the warpgroups share them.
+    static constexpr int REGS_LAUNCH = D == 64 ? 80 : 168, REGS_CTL = D == 64 ? 32 : 80, REGS_SOFT = D == 64 ? 104 : 208;
+    static constexpr int REGS_SPLIT = 128 * (REGS_CTL + 2 * REGS_SOFT);
+    static_assert(REGS_SPLIT <= 384 * REGS_LAUNCH, "register split exceeds the launch allocation");
 };
+constexpr int kFwdTcThreads = 384;
 
 struct FwdTcCtrl {
-    uint64_t kv_full[10], kv_empty[10];
+    uint64_t kv_full[8], kv_empty[8];
     uint64_t q_ready, tail_ready, mma_done;
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
@@ -87,16 +99,14 @@ struct FwdTcCtrl {
 };
 static_assert(sizeof(FwdTcCtrl) <= 2048, "control block too large");
 
-constexpr int kFwdTcThreads = 384;
-constexpr int kFwdTcRegsLaunch = 168, kFwdTcRegsCtl = 80, kFwdTcRegsSoft = 208;
-constexpr int kFwdTcRegsSplitTotal = 128 * (kFwdTcRegsCtl + 2 * kFwdTcRegsSoft);
-static_assert(kFwdTcRegsSplitTotal <= kFwdTcThreads * kFwdTcRegsLaunch, "register split exceeds the launch allocation");
 constexpr float kRiseLog2 = 8.0f;
 
 // Grid: row tiles (fastest), then splits, then PB * Hkv.
 template <int D, int kByKeys>
-__global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __grid_constant__ TcFwdArgs g) {
-    using L = FwdTcLayout<D>;
+__global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCKS_PER_SM))
+    attn_fwd_tc_kernel(const __grid_constant__ TcFwdArgs g) {
+    using L = FwdTcLayout<D, kByKeys>;
+    constexpr int KT = L::KT;
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (ptx::smem_u32(smem_raw) & 1023u)) & 1023u);
     FwdTcCtrl* ctrl = reinterpret_cast<FwdTcCtrl*>(smem + L::OFF_CTRL);
@@ -114,10 +124,10 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
 
     // This block's key tiles [t0, t0 + T) of the segments' tiles in a row.
     const int len0 = g.seg[0].length(pb), len1 = g.nseg > 1 ? g.seg[1].length(pb) : 0;
-    const int tiles0 = (len0 + 127) / 128;
+    const int tiles0 = (len0 + KT - 1) / KT;
     int t0, T;
     {
-        const long long all = static_cast<long long>(tiles0) + (len1 + 127) / 128;
+        const long long all = static_cast<long long>(tiles0) + (len1 + KT - 1) / KT;
         t0 = static_cast<int>(all * split / g.splits);
         T = static_cast<int>(all * (split + 1) / g.splits) - t0;
     }
@@ -128,8 +138,8 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     auto tile_of = [&](int t, int i) { return t0 + (kByKeys ? 2 * t + i : t); };
     // Segment and first key of a tile.
     auto seg_of = [&](int tile) { return tile < tiles0 ? 0 : 1; };
-    auto key_of = [&](int tile) { return (tile < tiles0 ? tile : tile - tiles0) * 128; };
-    auto is_tail = [&](int tile) { return (tile < tiles0 ? len0 : len1) - key_of(tile) < 128; };
+    auto key_of = [&](int tile) { return (tile < tiles0 ? tile : tile - tiles0) * KT; };
+    auto is_tail = [&](int tile) { return (tile < tiles0 ? len0 : len1) - key_of(tile) < KT; };
     constexpr int kTiles = kByKeys ? 2 : 1;  // K (and V) tiles of a step
 
     if (threadIdx.x == 0) {
@@ -154,7 +164,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             ptx::prefetch_tensormap(&g.seg[s].v);
         }
     if (warp == 1) {
-        ptx::tmem_alloc(&ctrl->tmem_base, 512);
+        ptx::tmem_alloc(&ctrl->tmem_base, L::TMEM_COLS);
         ptx::tmem_relinquish();
     }
     ptx::tc_fence_before();
@@ -164,7 +174,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     const uint64_t lim = g.wait_ns, dlim = g.drain_ns;
 
     if (warp < 4) {
-      ptx::regs_dec<kFwdTcRegsCtl>();
+      ptx::regs_dec<L::REGS_CTL>();
       if (warp == 0) {
         // ------------------------------------------------------------ producer
         // Ring order: the K tiles of step 0, its V tiles, the K tiles of step 1, ...
@@ -182,10 +192,10 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                 if (lane == 0) {
                     const int tile = tile_of(t, i);
                     const TcSeg& seg = g.seg[seg_of(tile)];
-                    uint8_t* dst = smem + L::OFF_KV + slot * L::TILE;
-                    ptx::mbar_arrive_expect_tx(&ctrl->kv_full[slot], L::TILE);
+                    uint8_t* dst = smem + L::OFF_KV + slot * L::KV_TILE;
+                    ptx::mbar_arrive_expect_tx(&ctrl->kv_full[slot], L::KV_TILE);
                     for (int c = 0; c < L::KC; ++c)
-                        tma_load_4d(dst + c * 16384, is_v ? &seg.v : &seg.k, &ctrl->kv_full[slot], c * 64,
+                        tma_load_4d(dst + c * KT * 128, is_v ? &seg.v : &seg.k, &ctrl->kv_full[slot], c * 64,
                                     key_of(tile), (is_v ? seg.vhead : seg.khead) ? hk : 0,
                                     (is_v ? seg.vbatch : seg.kbatch) ? pb : 0);
                 }
@@ -196,10 +206,10 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                     ok = mbar_wait(&ctrl->kv_full[slot], round & 1, abort_flag, lim, &g_lard_fault, kFaultFwdProducer);
                     ok = __all_sync(0xffffffffu, ok);
                     if (!ok) break;
-                    uint8_t* v = smem + L::OFF_KV + slot * L::TILE;
-                    for (int e = ((seg_of(tile) ? len1 : len0) - key_of(tile)) * 8 + lane; e < 1024; e += 32)
+                    uint8_t* v = smem + L::OFF_KV + slot * L::KV_TILE;
+                    for (int e = ((seg_of(tile) ? len1 : len0) - key_of(tile)) * 8 + lane; e < KT * 8; e += 32)
                         for (int c = 0; c < L::KC; ++c)
-                            *reinterpret_cast<uint4*>(v + c * 16384 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                            *reinterpret_cast<uint4*>(v + c * KT * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ptx::mbar_arrive(&ctrl->tail_ready);
@@ -217,7 +227,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         // One thread, and little else in its loop than waits and products: what
         // it does between them, the tensor pipe waits for.
         if (lane == 0) {
-            constexpr uint32_t kIdescS = ptx::idesc_bf16(128, 128, 0, 0);
+            constexpr uint32_t kIdescS = ptx::idesc_bf16(128, KT, 0, 0);
             constexpr uint32_t kIdescO = ptx::idesc_bf16(128, D, 0, 1);
             constexpr uint32_t kHi = ptx::sdesc_hi(1024);
             const uint32_t q_lo = ptx::sdesc_lo(ptx::smem_u32(smem + L::OFF_Q), 16);
@@ -241,8 +251,8 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             auto release = [&](const Place& x) { ptx::umma_commit(&ctrl->kv_empty[x.slot]); };
             auto issue_s = [&](int i, const Place& x) {  // S_i = Q_i K^T; Q is one tile by keys
                 const uint32_t a = q_lo + (kByKeys ? 0 : i * (L::TILE >> 4));
-                const uint32_t b = kv_k + x.slot * (L::TILE >> 4);
-                const uint32_t d = tmem + i * 128;
+                const uint32_t b = kv_k + x.slot * (L::KV_TILE >> 4);
+                const uint32_t d = tmem + i * KT;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     if (kk == 0) ptx::umma_ss<0>(d, a, b, kHi, kIdescS);
@@ -251,11 +261,11 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
                 ptx::umma_commit(&ctrl->s_full[i]);
             };
             auto issue_o = [&](int i, const Place& x, bool first) {  // O_i (+)= P_i V
-                const uint32_t a = tmem + i * 128, b = kv_mn + x.slot * (L::TILE >> 4);
-                const uint32_t d = tmem + 256 + i * 128;
+                const uint32_t a = tmem + i * KT, b = kv_mn + x.slot * (L::KV_TILE >> 4);
+                const uint32_t d = tmem + L::TMEM_O + i * L::TMEM_O_STEP;
                 umma_ts_acc(d, a, b, kHi, kIdescO, first ? 0u : 1u);
 #pragma unroll
-                for (int kk = 1; kk < 8; ++kk) ptx::umma_ts<1>(d, a + kk * 8, b + ptx::desc_step_mn(kk), kHi, kIdescO);
+                for (int kk = 1; kk < KT / 16; ++kk) ptx::umma_ts<1>(d, a + kk * 8, b + ptx::desc_step_mn(kk), kHi, kIdescO);
                 ptx::umma_commit(&ctrl->o_full[i]);
             };
             // Ring order: step by step the K tiles, then the V tiles; by keys an
@@ -315,7 +325,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         __syncwarp();
       }
     } else {
-        ptx::regs_inc<kFwdTcRegsSoft>();
+        ptx::regs_inc<L::REGS_SOFT>();
         // ------------------------------------------------------------ softmax
         const int q4 = warp & 3;
         const int i = (warp - 4) >> 2;  // stream
@@ -335,7 +345,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ctrl->q_ready);
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
-        const uint32_t ts = lane_base + i * 128, to = lane_base + 256 + i * 128;
+        const uint32_t ts = lane_base + i * KT, to = lane_base + L::TMEM_O + i * L::TMEM_O_STEP;
         const float cf = g.cfac;
         float m = -INFINITY, l = 0.f;  // reference (log2 domain) and sum of 2^(z - m)
         const int mine = steps(i);
@@ -348,24 +358,25 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             ptx::tc_fence_after();
-            float z[4][32];
+            float z[KT / 32][32];
             __syncwarp();
 #pragma unroll
-            for (int c = 0; c < 4; ++c) ptx::tmem_ld32(ts + c * 32, z[c]);
+            for (int c = 0; c < KT / 32; ++c) ptx::tmem_ld32(ts + c * 32, z[c]);
             ptx::tmem_ld_wait(z[0]);
 #pragma unroll
-            for (int c = 1; c < 4; ++c) ptx::reg_dep(z[c]);
-            if (lim_keys < 128) {
+            for (int c = 1; c < KT / 32; ++c) ptx::reg_dep(z[c]);
+            if (lim_keys < KT) {
 #pragma unroll
-                for (int c = 0; c < 128; ++c)
+                for (int c = 0; c < KT; ++c)
                     if (c >= lim_keys) z[c >> 5][c & 31] = -INFINITY;
             }
-            float top[4];
+            float top[4];  // of four runs of columns, side by side
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
-                top[c] = fmaxf(z[c][0], z[c][1]);
+                constexpr int kRun = KT / 4;
+                top[c] = fmaxf(z[c * kRun >> 5][c * kRun & 31], z[c * kRun >> 5][(c * kRun & 31) + 1]);
 #pragma unroll
-                for (int k = 2; k < 32; k += 2) top[c] = ptx::fmax3(top[c], z[c][k], z[c][k + 1]);
+                for (int k = c * kRun + 2; k < (c + 1) * kRun; k += 2) top[c] = ptx::fmax3(top[c], z[k >> 5][k & 31], z[k >> 5][(k & 31) + 1]);
             }
             const float mx = fmaxf(ptx::fmax3(top[0], top[1], top[2]), top[3]) * cf;
             const bool rise = mx > m + kRiseLog2;  // always where the row has seen nothing yet and now does
@@ -395,7 +406,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
             const float2 cf2 = splat2(cf), nb2 = splat2(-base);
             float2 sum = splat2(0.f);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            for (int h = 0; h < KT / 64; ++h) {
                 uint32_t pk[32];
 #pragma unroll
                 for (int k = 0; k < 64; k += 2) {
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, 1) attn_fwd_tc_kernel(const __g
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    if (warp == 1) ptx::tmem_dealloc(tmem, 512);
+    if (warp == 1) ptx::tmem_dealloc(tmem, L::TMEM_COLS);
     if (g.second) wait_for_kernel_before();  // whoever waits for this pass has waited for the first
 }
 

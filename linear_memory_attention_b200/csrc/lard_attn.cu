@@ -63,8 +63,8 @@ lard_status setup_device(int dev) {
         };
         auto tc_d = [&](auto d) {
             constexpr int D = decltype(d)::value;
-            tc(attn_fwd_tc_kernel<D, 0>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
-            tc(attn_fwd_tc_kernel<D, 1>, FwdTcLayout<D>::SMEM_BYTES, kFwdTcThreads, kFwdTcRegsSplitTotal);
+            tc(attn_fwd_tc_kernel<D, 0>, FwdTcLayout<D, 0>::SMEM_BYTES, kFwdTcThreads, FwdTcLayout<D, 0>::REGS_SPLIT);
+            tc(attn_fwd_tc_kernel<D, 1>, FwdTcLayout<D, 1>::SMEM_BYTES, kFwdTcThreads, FwdTcLayout<D, 1>::REGS_SPLIT);
             ok = ok && set_smem(attn_few_kernel<D>, FewLayout<D>::SMEM_BYTES) == cudaSuccess;
             tc(attn_dq_tc_kernel<D>, DqLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
             tc(attn_dkdv_tc_kernel<D>, DkvLayout<D>::SMEM_BYTES, kBwdTcThreads, kDqRegsSplitTotal);
@@ -295,31 +295,35 @@ Pass plan_simt(long long problems, long long R, int d, long long tiles) {
     return p;
 }
 
+// Keys of a tile of the tensor-core pass.
+int tc_tile(int d) { return d == 64 ? lard::attn::FwdTcLayout<64, 0>::KT : lard::attn::FwdTcLayout<128, 0>::KT; }
+
 // Tensor-core pass.  Up to 128 rows the two streams of a block share them and
 // take alternate key tiles; more rows take one tile of rows each.  The number
 // of splits is the one that a model of the pass's time gives, in cycles: a
-// step (products and exponentials of two tiles) takes 3700, or as long as HBM
-// (3400 B a cycle) needs to bring the running blocks' tiles where each is read
-// once; a block's beginning and end 12000; partial rows are written, read and
-// joined at 3400 B a cycle by a kernel of its own, 8000.
+// step (products and exponentials of two tiles) takes 3700 (d = 64: 2 x 64 keys, two blocks
+// an SM), or as long as HBM (3400 B a cycle) needs to bring the
+// running blocks' tiles where each is read once; a block's beginning and end
+// 12000; partial rows are written, read and joined at 3400 B a cycle by a
+// kernel of its own, 8000.
 // (1 x 4096 rows of 32 heads over 16384 keys, 512 blocks: one split 1.10 ms, two 1.06 ms.)
 Pass plan_tc(long long problems, long long R, int d, long long tiles, long long rows) {
     Pass p;
     const bool by_keys = R <= 128;
     p.kind = by_keys ? Pass::kTcKeys : Pass::kTcRows;
-    const long long rtiles = tiles_of(R, by_keys ? 128 : 256);
+    const long long rtiles = tiles_of(R, by_keys ? 128 : 256), slots = d == 64 ? 2 * kSms : kSms;
     p.blocks = problems * rtiles;
     double best = 0.0;
     const long long most = std::max(1LL, std::min(64LL, by_keys ? tiles / 2 : tiles));
     for (long long s = 1; s <= most; ++s) {
-        const long long blocks = p.blocks * s, full = blocks / kSms, rest = blocks % kSms;
+        const long long blocks = p.blocks * s, full = blocks / slots, rest = blocks % slots;
         const double steps = static_cast<double>(tiles_of(tiles_of(tiles, s), by_keys ? 2 : 1));
         auto time = [&](long long running) {
             double step = 3700.0;
-            if (rtiles == 1) step = std::max(step, (by_keys ? 2 : 1) * 512.0 * d * running / 3400.0);
+            if (rtiles == 1) step = std::max(step, (by_keys ? 2 : 1) * 4.0 * tc_tile(d) * d * running / 3400.0);
             return steps * step + 12000.0;
         };
-        double cost = full * time(kSms) + (rest ? time(rest) : 0.0);
+        double cost = full * time(slots) + (rest ? time(rest) : 0.0);
         if (s > 1) cost += 8000.0 + 8.0 * s * rows * d / 3400.0;
         if (s == 1 || cost < best) {
             best = cost;
@@ -394,7 +398,7 @@ FwdPlan plan_fwd(const Fwd& f) {
         };
         Pass x = fp32                         ? plan_simt(problems, R, f.d, tiles(lard::attn::kSimtTile))
                  : R <= lard::attn::kFewRows ? plan_few(problems, tiles(16), f.d)
-                                              : plan_tc(problems, R, f.d, tiles(128), p.rows);
+                                              : plan_tc(problems, R, f.d, tiles(tc_tile(f.d)), p.rows);
         x.seg = seg;
         x.nseg = nseg;
         x.shared = shared;
@@ -526,11 +530,13 @@ lard_status run_tc(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, co
     using namespace lard::attn;
     TcFwdArgs a;
     pass_args(a, f, p, x, split0, g);
-    if (!make_segs(a.seg, f, x, 128)) return LARD_ERR_INVALID_ARG;
+    if (!make_segs(a.seg, f, x, FwdTcLayout<D, 0>::KT)) return LARD_ERR_INVALID_ARG;
     a.wait_ns = kWaitLimitNs;
     a.drain_ns = kDrainLimitNs;
-    return launch(x.kind == Pass::kTcKeys ? attn_fwd_tc_kernel<D, 1> : attn_fwd_tc_kernel<D, 0>, x.blocks * x.splits,
-                  kFwdTcThreads, FwdTcLayout<D>::SMEM_BYTES, stream, a.second, 0, a);
+    return x.kind == Pass::kTcKeys ? launch(attn_fwd_tc_kernel<D, 1>, x.blocks * x.splits, kFwdTcThreads,
+                                            FwdTcLayout<D, 1>::SMEM_BYTES, stream, a.second, 0, a)
+                                   : launch(attn_fwd_tc_kernel<D, 0>, x.blocks * x.splits, kFwdTcThreads,
+                                            FwdTcLayout<D, 0>::SMEM_BYTES, stream, a.second, 0, a);
 }
 
 template <typename T, int D>
