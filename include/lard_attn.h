@@ -29,8 +29,8 @@
  *   - Inputs and outputs are bf16 (LARD_DTYPE_BF16) or fp32 (LARD_DTYPE_FP32),
  *     one type per call; d is 64 or 128.  LSE is fp32, contiguous [B, Hq, n].
  *     Products, softmax statistics and sums are held in fp32; for bf16 the
- *     probabilities (and dZ) are rounded to bf16 where they enter a product,
- *     every output is rounded once.
+ *     probabilities (and dZ) are rounded to bf16 where they enter a product, and
+ *     delta is formed from the rounded out; every output is rounded once.
  *   - Lengths (k_len, s_len) are int32 in device memory, so that a captured
  *     graph can be replayed with other lengths; a length outside [0, rows] counts
  *     as the nearer bound.  Key and value rows at or past their sequence's length are not used:
@@ -95,7 +95,7 @@ LARD_API size_t lard_cross_attn_bwd_workspace_bytes(const lard_cross_attn* a);
 LARD_API lard_status lard_cross_attn_fwd(const lard_cross_attn* a, void* workspace, size_t workspace_bytes,
                                          cudaStream_t stream);
 
-/* Writes dq, dk and dv, given what lard_cross_attn_fwd wrote for the same inputs. */
+/* Writes dq, dk and dv, given what lard_cross_attn_fwd wrote for the same inputs.  Deterministic. */
 LARD_API lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_t workspace_bytes,
                                          cudaStream_t stream);
 

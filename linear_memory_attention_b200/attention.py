@@ -97,16 +97,20 @@ def _refuse(t, shape, dtype, q, name):
 def _view(t, shape, q, name):
     """The fields of a lard_attn_view of t [B, H, rows, d], which must have this shape and q's
     dtype and device."""
+    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device():
+        _refuse(t, shape, q.dtype, q, name)
     batch, head, row, one = t.stride()
-    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device() or one != 1:
+    if one != 1:
         _refuse(t, shape, q.dtype, q, name)
     return t.data_ptr(), batch, head, row
 
 
 def _shared(t, shape, q, name):
     """The fields of a lard_attn_view of t [H, rows, d], one block for all sequences."""
+    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device():
+        _refuse(t, shape, q.dtype, q, name)
     head, row, one = t.stride()
-    if t.shape != shape or t.dtype is not q.dtype or t.get_device() != q.get_device() or one != 1:
+    if one != 1:
         _refuse(t, shape, q.dtype, q, name)
     return t.data_ptr(), 0, head, row
 
