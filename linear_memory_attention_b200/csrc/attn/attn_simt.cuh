@@ -26,7 +26,7 @@
 namespace lard {
 namespace attn {
 
-constexpr int kSimtGroup = 128, kSimtThreads = 2 * kSimtGroup;
+constexpr int kSimtGroup = 256, kSimtThreads = 2 * kSimtGroup;
 constexpr int kSimtTile = 64;  // rows and keys of a tile
 constexpr int kSimtPStride = 68;
 
@@ -142,7 +142,7 @@ template <int D, int RT>
 __global__ void __launch_bounds__(kSimtThreads) attn_fwd_simt_kernel(const __grid_constant__ FwdArgs<float> g) {
     using L = SimtLayout<D>;
     if (g.join) next_may_start();
-    constexpr int kRows = 8 * RT;
+    constexpr int kRows = kSimtGroup / 16 * RT;
     extern __shared__ float4 smem4[];
     const int grp = threadIdx.x / kSimtGroup, me = threadIdx.x % kSimtGroup;
     float* qs = reinterpret_cast<float*>(smem4);
@@ -307,7 +307,7 @@ template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_dq_simt_kernel(const __grid_constant__ SimtBwdArgs g) {
     using L = SimtLayout<D>;
     next_may_start();
-    constexpr int RT = 8;
+    constexpr int RT = 4;
     extern __shared__ float4 smem4[];
     float* qs = reinterpret_cast<float*>(smem4);
     float* os = qs + L::TILE;
@@ -436,7 +436,7 @@ template <int D>
 __global__ void __launch_bounds__(kSimtThreads) attn_dkdv_simt_kernel(const __grid_constant__ SimtBwdArgs g) {
     using L = SimtLayout<D>;
     if (g.qsplits > 1 || g.ksplits > 1) next_may_start();
-    constexpr int RT = 8;
+    constexpr int RT = 4;
     extern __shared__ float4 smem4[];
     float* ks = reinterpret_cast<float*>(smem4);
     float* vs = ks + L::TILE;

@@ -73,8 +73,8 @@ lard_status setup_device(int dev) {
         tc_d(std::integral_constant<int, 128>());
         auto simt = [&](auto d) {
             constexpr int D = decltype(d)::value;
-            ok = ok && set_smem(attn_fwd_simt_kernel<D, 2>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
-                 set_smem(attn_fwd_simt_kernel<D, 8>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
+            ok = ok && set_smem(attn_fwd_simt_kernel<D, 1>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
+                 set_smem(attn_fwd_simt_kernel<D, 4>, SimtLayout<D>::FWD_BYTES) == cudaSuccess &&
                  set_smem(attn_dkdv_simt_kernel<D>, SimtLayout<D>::DKDV_BYTES) == cudaSuccess &&
                  set_smem(attn_dq_simt_kernel<D>, SimtLayout<D>::DQ_BYTES) == cudaSuccess;
         };
@@ -486,7 +486,7 @@ lard_status run_simt(const Fwd& f, const FwdPlan& p, const Pass& x, int split0, 
     pass_args(a, f, p, x, split0, g);
     a.seg[0] = g.seg[x.seg];
     a.seg[1] = g.seg[x.nseg > 1 ? x.seg + 1 : x.seg];
-    return launch(x.kind == Pass::kSimtFew ? attn_fwd_simt_kernel<D, 2> : attn_fwd_simt_kernel<D, 8>, x.blocks * x.splits,
+    return launch(x.kind == Pass::kSimtFew ? attn_fwd_simt_kernel<D, 1> : attn_fwd_simt_kernel<D, 4>, x.blocks * x.splits,
                   kSimtThreads, SimtLayout<D>::FWD_BYTES, stream, a.second, 0, a);
 }
 
