@@ -137,5 +137,30 @@ __device__ __forceinline__ void staged_rows_out(uint32_t stage, void* mine, int 
     __syncwarp();  // the area may be written again
 }
 
+// Rounds 32 fp32 columns, times `scale`, to bf16 into units first and up of a staged row of ROW bytes.
+template <int ROW>
+__device__ __forceinline__ void stage_bf16(uint32_t area, int lane, int first, const float (&o)[32], float scale) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+        ptx::st_shared_v4(stage_unit<ROW>(area, lane, first + u), ptx::pack_bf16x2(o[8 * u] * scale, o[8 * u + 1] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 2] * scale, o[8 * u + 3] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 4] * scale, o[8 * u + 5] * scale),
+                          ptx::pack_bf16x2(o[8 * u + 6] * scale, o[8 * u + 7] * scale));
+}
+
+// Writes 32 fp32 columns of a warp's 32 rows, COLS at a time through the area.
+template <int COLS>
+__device__ __forceinline__ void fp32_rows_out(uint32_t area, int lane, const float (&o)[32], float* mine) {
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
+#pragma unroll
+    for (int x = 0; x < 32; x += COLS) {
+#pragma unroll
+        for (int u = 0; u < COLS / 4; ++u)
+            ptx::st_shared_v4(stage_unit<COLS * 4>(area, lane, u), w[x + 4 * u], w[x + 4 * u + 1], w[x + 4 * u + 2],
+                              w[x + 4 * u + 3]);
+        staged_rows_out<COLS * 4>(area, mine ? mine + x : nullptr, lane);
+    }
+}
+
 }  // namespace attn
 }  // namespace lard

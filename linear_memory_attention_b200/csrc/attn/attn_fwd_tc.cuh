@@ -77,7 +77,7 @@ struct FwdTcLayout {
     static constexpr int OFF_CTRL = OFF_KV + NS * KV_TILE;
     static constexpr int SMEM_BYTES = OFF_CTRL + 2048 + 1024;
     // By keys, the join stages a stream's O in the ring: 128 x D fp32.
-    static_assert(!kByKeys || NS * KV_TILE >= 128 * D * 4, "no room for the join");
+    static_assert(!kByKeys || NS * KV_TILE >= 128 * (D + 4) * 4, "no room for the join");
     static_assert(BLOCKS_PER_SM * (SMEM_BYTES + 1024) <= 233472, "too much shared memory");
     // Tensor memory: S of stream i at KT i, O at TMEM_O + TMEM_O_STEP i.
     static constexpr int TMEM_COLS = 512 / BLOCKS_PER_SM, TMEM_O = TMEM_COLS / 2, TMEM_O_STEP = TMEM_COLS / 4;
@@ -95,7 +95,6 @@ struct FwdTcCtrl {
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
     int abort_flag;
-    float join_m[128], join_l[128];
 };
 static_assert(sizeof(FwdTcCtrl) <= 2048, "control block too large");
 
@@ -432,53 +431,54 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             ptx::tc_fence_after();
         }
         float* stage = reinterpret_cast<float*>(smem + L::OFF_KV);  // [D][128], the ring is empty by then
+        float* stats = stage + D * 128;                              // [stream][m, l][128]
         float w0 = 1.f, w1 = 0.f, m_all = m, l_all = l;
         if (kByKeys) {
-            // Stream 1 leaves its rows, stream 0 joins them to its own.  Stream 1's
-            // last product is the ring's last reader but for stream 0's, whose
-            // threads wait for theirs before the first barrier.
+            // Each stream leaves half of its columns and brings the other half home,
+            // joined.  Its last product has read the ring for the last time, and
+            // either waits for the other's at the first barrier.
             ptx::named_bar_sync(1, 256);
-            if (i == 1) {
-                ctrl->join_m[row] = m;
-                ctrl->join_l[row] = l;
-                if (ok && mine > 0) {
+            stats[256 * i + row] = m;
+            stats[256 * i + 128 + row] = l;
+            if (ok && mine > 0) {
 #pragma unroll
-                    for (int c = 0; c < D; c += 32) {
-                        float o[32];
-                        __syncwarp();
-                        ptx::tmem_ld32(to + c, o);
-                        ptx::tmem_ld_wait(o);
+                for (int c = 0; c < D / 2; c += 32) {
+                    const int col = (1 - i) * (D / 2) + c;
+                    float o[32];
+                    __syncwarp();
+                    ptx::tmem_ld32(to + col, o);
+                    ptx::tmem_ld_wait(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) stage[(c + k) * 128 + row] = o[k];
-                    }
+                    for (int k = 0; k < 32; ++k) stage[(col + k) * 128 + row] = o[k];
                 }
             }
             ptx::named_bar_sync(1, 256);
-            if (i == 0) {
-                const float m1 = ctrl->join_m[row];
-                m_all = fmaxf(m, m1);
-                const float base = m_all == -INFINITY ? 0.f : m_all;
-                w0 = ptx::ex2(m - base);
-                w1 = ptx::ex2(m1 - base);
-                l_all = l * w0 + ctrl->join_l[row] * w1;
-            }
+            const float m1 = stats[256 * (1 - i) + row];
+            m_all = fmaxf(m, m1);
+            const float base = m_all == -INFINITY ? 0.f : m_all;
+            w0 = ptx::ex2(m - base);
+            w1 = ptx::ex2(m1 - base);
+            l_all = l * w0 + stats[256 * (1 - i) + 128 + row] * w1;
         }
-        if (ok && !*abort_flag && (!kByKeys || i == 0)) {
+        if (ok && !*abort_flag) {
             const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
             w0 *= inv;
             w1 *= inv;
             const float lse = l_all == 0.f ? -INFINITY : (m_all + log2f(l_all)) * kLn2;
             const long long grow = (static_cast<long long>(b) * g.Hkv + hk) * Gn + rem;
             const long long prow = (g.split0 + split) * g.rows + grow;
-            const bool second = kByKeys && steps(1) > 0;
-            // Through this warp's rows of Q's tile, which the last S has read, to memory.
-            const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE) + q4 * (L::TILE / 4);
+            const bool other = kByKeys && steps(1 - i) > 0;
+            // This thread's columns [col0, col0 + kCols), through the warp's share of Q's
+            // tile, which the last S has read, to memory.
+            constexpr int kCols = kByKeys ? D / 2 : D, kPart = kByKeys ? D / 4 : 32;
+            const int col0 = kByKeys ? i * (D / 2) : 0;
+            const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? (4 * i + q4) * (L::TILE / 8) : i * L::TILE + q4 * (L::TILE / 4));
 #pragma unroll
-            for (int c = 0; c < D; c += 32) {
+            for (int c = 0; c < kCols; c += 32) {
                 float o[32];
                 __syncwarp();
                 if (mine > 0) {
-                    ptx::tmem_ld32(to + c, o);
+                    ptx::tmem_ld32(to + col0 + c, o);
                     ptx::tmem_ld_wait(o);
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] *= w0;
@@ -486,26 +486,17 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                if (second) {
+                if (other) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(c + k) * 128 + row], w1, o[k]);
+                    for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(col0 + c + k) * 128 + row], w1, o[k]);
                 }
-                if (g.join) {  // 32 columns of fp32
-                    const uint32_t* w = reinterpret_cast<const uint32_t*>(o);
-#pragma unroll
-                    for (int u = 0; u < 8; ++u)
-                        ptx::st_shared_v4(stage_unit<128>(area, lane, u), w[4 * u], w[4 * u + 1], w[4 * u + 2], w[4 * u + 3]);
-                    staged_rows_out<128>(area, row_ok ? g.part_o + prow * D + c : nullptr, lane);
-                } else {
-#pragma unroll
-                    for (int u = 0; u < 4; ++u)
-                        ptx::st_shared_v4(stage_unit<D * 2>(area, lane, c / 8 + u), ptx::pack_bf16x2(o[8 * u], o[8 * u + 1]),
-                                          ptx::pack_bf16x2(o[8 * u + 2], o[8 * u + 3]), ptx::pack_bf16x2(o[8 * u + 4], o[8 * u + 5]),
-                                          ptx::pack_bf16x2(o[8 * u + 6], o[8 * u + 7]));
-                }
+                if (g.join)
+                    fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + col0 + c : nullptr);
+                else
+                    stage_bf16<kCols * 2>(area, lane, c / 8, o, 1.f);
             }
-            if (!g.join) staged_rows_out<D * 2>(area, row_ok ? g.out.row(b, head, pos) : nullptr, lane);
-            if (row_ok) {
+            if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? g.out.row(b, head, pos) + col0 : nullptr, lane);
+            if (row_ok && (!kByKeys || i == 0)) {
                 if (g.join) g.part_lse[prow] = lse;
                 else g.lse[grow] = lse;
             }
