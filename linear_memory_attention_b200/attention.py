@@ -4,9 +4,10 @@ cross attention and attention over a shared prefix.
 Argument marshalling only, as in ``lard``: every step of the computation runs in the
 library's kernels, and importing this module fails loudly if the library has not been
 built.  Functions with the C names take the caller's buffers:
-    lard_cross_attn_fwd(q, k, v, tau, out, lse, k_len=None, workspace=None, stream=None)
+    lard_cross_attn_fwd(q, k, v, tau, out, lse, k_len=None, workspace=None, stream=None,
+                        rest=None)
     lard_cross_attn_bwd(q, k, v, tau, out, lse, dout, dq, dk, dv, k_len=None,
-                        workspace=None, stream=None)
+                        workspace=None, stream=None, rest=None)
     lard_prefix_attn(q, kp, vp, ks, vs, s_len, tau, out, lse, workspace=None, stream=None)
     lard_cross_attn_fwd_workspace_bytes(q, k), lard_cross_attn_bwd_workspace_bytes(q, k),
     lard_prefix_attn_workspace_bytes(q, kp, ks) -> bytes
@@ -37,7 +38,7 @@ EXPORTS = ("lard_cross_attn_fwd_workspace_bytes", "lard_cross_attn_bwd_workspace
 
 # struct lard_cross_attn and lard_prefix_attn_args, packed in one go: seven ints and a
 # float, then 8-byte fields (a view is a pointer and three strides).
-_CROSS = struct.Struct("7if" + "4q" * 3 + "q" + "4q" + "q" + "4q" * 4)
+_CROSS = struct.Struct("7if" + "4q" * 3 + "q" + "4q" + "q" + "4q" * 5)
 _PREFIX = struct.Struct("8if4x" + "4q" * 5 + "q" + "4q" + "q")
 _NO_VIEW = (0, 0, 0, 0)
 _NO_GRADS = _NO_VIEW * 4
@@ -159,7 +160,7 @@ def _cross_sizes(q, k):
 
 
 def _cross_bytes(fn, sizes):
-    return fn(_CROSS.pack(*sizes, 1.0, *_NO_VIEW * 3, 0, *_NO_VIEW, 0, *_NO_VIEW * 4))
+    return fn(_CROSS.pack(*sizes, 1.0, *_NO_VIEW * 3, 0, *_NO_VIEW, 0, *_NO_GRADS, *_NO_VIEW))
 
 
 def lard_cross_attn_fwd_workspace_bytes(q, k) -> int:
@@ -172,7 +173,7 @@ def lard_cross_attn_bwd_workspace_bytes(q, k) -> int:
     return _cross_bytes(_lib.lard_cross_attn_bwd_workspace_bytes, _cross_sizes(q, k))
 
 
-def _cross_args(q, k, v, tau, k_len, out, lse, grads=None):
+def _cross_args(q, k, v, tau, k_len, out, lse, grads=None, rest=None):
     sizes = _cross_sizes(q, k)
     _, B, Hq, Hkv, n, m, d = sizes
     qs, ks = (B, Hq, n, d), (B, Hkv, m, d)
@@ -183,21 +184,24 @@ def _cross_args(q, k, v, tau, k_len, out, lse, grads=None):
                       *_view(dv, ks, q, "dv"))
     return _CROSS.pack(*sizes, tau, *_view(q, qs, q, "q"), *_view(k, ks, q, "k"), *_view(v, ks, q, "v"),
                        0 if k_len is None else _flat(k_len, (B,), torch.int32, q, "k_len"),
-                       *_view(out, qs, q, "out"), _flat(lse, (B, Hq, n), torch.float32, q, "lse"), *grad_views)
+                       *_view(out, qs, q, "out"), _flat(lse, (B, Hq, n), torch.float32, q, "lse"), *grad_views,
+                       *(_NO_VIEW if rest is None else _view(rest, qs, q, "rest")))
 
 
-def lard_cross_attn_fwd(q, k, v, tau, out, lse, k_len=None, workspace=None, stream=None):
+def lard_cross_attn_fwd(q, k, v, tau, out, lse, k_len=None, workspace=None, stream=None, rest=None):
     """Cross attention: writes out [B, Hq, n, d] and lse [B, Hq, n] (fp32) of queries q
-    [B, Hq, n, d] over k, v [B, Hkv, m, d], of which sequence b has k_len[b] rows (int32)."""
-    args = _cross_args(q, k, v, tau, k_len, out, lse)
+    [B, Hq, n, d] over k, v [B, Hkv, m, d], of which sequence b has k_len[b] rows (int32).  rest (bf16, like out):
+    takes what rounding left of out, for the backward pass."""
+    args = _cross_args(q, k, v, tau, k_len, out, lse, None, rest)
     need = _lib.lard_cross_attn_fwd_workspace_bytes(args)
     _call(_lib.lard_cross_attn_fwd, "lard_cross_attn_fwd", args, workspace, need, q, stream)
 
 
-def lard_cross_attn_bwd(q, k, v, tau, out, lse, dout, dq, dk, dv, k_len=None, workspace=None, stream=None):
+def lard_cross_attn_bwd(q, k, v, tau, out, lse, dout, dq, dk, dv, k_len=None, workspace=None, stream=None,
+                        rest=None):
     """Gradients of cross attention: writes dq, dk and dv for the upstream gradient dout, given
-    out and lse of lard_cross_attn_fwd on the same inputs."""
-    args = _cross_args(q, k, v, tau, k_len, out, lse, (dout, dq, dk, dv))
+    out, lse and (where it was taken) rest of lard_cross_attn_fwd on the same inputs."""
+    args = _cross_args(q, k, v, tau, k_len, out, lse, (dout, dq, dk, dv), rest)
     need = _lib.lard_cross_attn_bwd_workspace_bytes(args)
     _call(_lib.lard_cross_attn_bwd, "lard_cross_attn_bwd", args, workspace, need, q, stream)
 
@@ -270,7 +274,8 @@ def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
         raise ValueError("q must be [B, H, rows, d]")
     out, lse = _outputs(q)
     grads = None if dout is None else (dout, torch.empty_like(q), torch.empty_like(k), torch.empty_like(v))
-    args = _cross_args(q, k, v, tau, k_len, out, lse, grads)
+    rest = torch.empty_like(q) if grads is not None and q.dtype is torch.bfloat16 else None
+    args = _cross_args(q, k, v, tau, k_len, out, lse, grads, rest)
     need = _lib.lard_cross_attn_fwd_workspace_bytes(args)
     _call(_lib.lard_cross_attn_fwd, "lard_cross_attn_fwd", args, _bytes(need, q), need, q, None)
     got = {"out": out, "lse": lse}

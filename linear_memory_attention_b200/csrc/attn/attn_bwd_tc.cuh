@@ -34,7 +34,7 @@ namespace attn {
 struct TcBwdArgs {
     CUtensorMap k, v;       // boxes of 128 rows
     CUtensorMap q64, do64;  // boxes of 64 rows (dK, dV)
-    View<const __nv_bfloat16> q, out, dout;
+    View<const __nv_bfloat16> q, out, rest, dout;  // rest.p may be NULL
     View<__nv_bfloat16> dq, dk, dv;
     const float* lse;
     float* delta;
@@ -270,18 +270,23 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
             copy_commit();
             constexpr int kLanes = D / 8;
             const __nv_bfloat16* oo = row_ok ? g.out.row(b, head, pos) : nullptr;
+            const __nv_bfloat16* orest = row_ok && g.rest.p ? g.rest.row(b, head, pos) : nullptr;
 #pragma unroll 4
             for (int k = 16 * half; k < 16 * half + 16; k += 32 / kLanes) {
                 const int x = k + lane / kLanes, u = lane % kLanes;
-                const __nv_bfloat16 *pd = shfl_ptr(od, x), *po = shfl_ptr(oo, x);
+                const __nv_bfloat16 *pd = shfl_ptr(od, x), *po = shfl_ptr(oo, x), *pr = shfl_ptr(orest, x);
                 float s = 0.f;
                 if (pd) {
                     const uint4 d4 = __ldg(reinterpret_cast<const uint4*>(pd) + u), o4 = __ldg(reinterpret_cast<const uint4*>(po) + u);
+                    uint4 r4 = make_uint4(0u, 0u, 0u, 0u);
+                    if (pr) r4 = __ldg(reinterpret_cast<const uint4*>(pr) + u);
                     const uint32_t xs[4] = {d4.x, d4.y, d4.z, d4.w}, ys[4] = {o4.x, o4.y, o4.z, o4.w};
+                    const uint32_t rs[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16), s);
-                        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u), __uint_as_float(ys[e] & 0xffff0000u), s);
+                        s = fmaf(__uint_as_float(xs[e] << 16), __uint_as_float(ys[e] << 16) + __uint_as_float(rs[e] << 16), s);
+                        s = fmaf(__uint_as_float(xs[e] & 0xffff0000u),
+                                 __uint_as_float(ys[e] & 0xffff0000u) + __uint_as_float(rs[e] & 0xffff0000u), s);
                     }
                 }
 #pragma unroll

@@ -45,8 +45,8 @@ struct KeySeg {
 template <typename T>
 struct FwdArgs {
     View<const T> q;
-    View<T> out;
-    float* lse;  // [B, Hq, n]
+    View<T> out, rest;  // rest: what rounding left of out, or p = NULL
+    float* lse;         // [B, Hq, n]
     KeySeg<T> seg[2];
     int nseg;
     int PB, Hkv, G, n, R;
@@ -147,6 +147,9 @@ __device__ __forceinline__ void stage_bf16(uint32_t area, int lane, int first, c
                           ptx::pack_bf16x2(o[8 * u + 4] * scale, o[8 * u + 5] * scale),
                           ptx::pack_bf16x2(o[8 * u + 6] * scale, o[8 * u + 7] * scale));
 }
+
+// What rounding to bf16 leaves of x.
+__device__ __forceinline__ float rounding_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
 
 // Writes 32 fp32 columns of a warp's 32 rows, COLS at a time through the area.
 template <int COLS>

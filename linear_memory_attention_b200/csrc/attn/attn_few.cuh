@@ -33,7 +33,7 @@ namespace attn {
 struct FewArgs {
     TcSeg seg[2];  // boxes of 16 rows
     View<const __nv_bfloat16> q;
-    View<__nv_bfloat16> out;
+    View<__nv_bfloat16> out, rest;
     float* lse;
     int nseg, PB, Hkv, G, n, R;  // as in TcFwdArgs; R <= 16
     int cluster, splits;         // blocks of a cluster; clusters of a problem
@@ -339,6 +339,9 @@ __global__ void __launch_bounds__(32 * kFewWarps, 3) attn_few_kernel(const __gri
         } else {
             const int b = pb + r / Gn, rem = r % Gn;
             store4(g.out.row(b, hk * g.G + rem / g.n, rem % g.n) + x, acc);
+            if (g.rest.p)
+                store4(g.rest.row(b, hk * g.G + rem / g.n, rem % g.n) + x,
+                       make_float4(rounding_rest(acc.x), rounding_rest(acc.y), rounding_rest(acc.z), rounding_rest(acc.w)));
             if (x == 0) g.lse[row] = lse;
         }
     }

@@ -51,7 +51,7 @@ struct TcSeg {
 struct TcFwdArgs {
     TcSeg seg[2];
     View<const __nv_bfloat16> q;
-    View<__nv_bfloat16> out;
+    View<__nv_bfloat16> out, rest;
     float* lse;  // [B, Hq, n]
     int nseg, PB, Hkv, G, n, R;
     int splits, split0;  // with join: partial rows go to split0 + split
@@ -473,6 +473,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             constexpr int kCols = kByKeys ? D / 2 : D, kPart = kByKeys ? D / 4 : 32;
             const int col0 = kByKeys ? i * (D / 2) : 0;
             const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? (4 * i + q4) * (L::TILE / 8) : i * L::TILE + q4 * (L::TILE / 4));
+            auto write = [&](bool rest) {
 #pragma unroll
             for (int c = 0; c < kCols; c += 32) {
                 float o[32];
@@ -490,12 +491,19 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
 #pragma unroll
                     for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(col0 + c + k) * 128 + row], w1, o[k]);
                 }
+                if (rest) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = rounding_rest(o[k]);
+                }
                 if (g.join)
                     fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + col0 + c : nullptr);
                 else
                     stage_bf16<kCols * 2>(area, lane, c / 8, o, 1.f);
             }
-            if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? g.out.row(b, head, pos) + col0 : nullptr, lane);
+            if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? (rest ? g.rest : g.out).row(b, head, pos) + col0 : nullptr, lane);
+            };
+            write(false);
+            if (g.rest.p && !g.join) write(true);
             if (row_ok && (!kByKeys || i == 0)) {
                 if (g.join) g.part_lse[prow] = lse;
                 else g.lse[grow] = lse;

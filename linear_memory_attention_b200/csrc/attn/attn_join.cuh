@@ -53,6 +53,11 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     T* dst = g.out.row(bh / g.Hkv, bh % g.Hkv * g.G + r / g.n, r % g.n) + lane * E;
 #pragma unroll
     for (int e = 0; e < E; ++e) dst[e] = static_cast<T>(o[e] * inv);
+    if (g.rest.p) {
+        T* rest = g.rest.row(bh / g.Hkv, bh % g.Hkv * g.G + r / g.n, r % g.n) + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) rest[e] = static_cast<T>(o[e] * inv - static_cast<float>(dst[e]));
+    }
     if (lane == 0) g.lse[row] = total == 0.f ? -INFINITY : base + log2f(total) * kLn2;
 }
 

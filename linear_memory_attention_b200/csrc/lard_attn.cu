@@ -286,12 +286,33 @@ int split_to_fill(long long blocks, long long steps, long long slots) {
     return static_cast<int>(std::max(1LL, std::min(steps, slots / blocks)));
 }
 
-// CUDA-core pass, in tiles of 64 rows, or of 16 where that is all there are.
+// The same for the CUDA-core kernels, whose blocks are few and long: the number
+// with the least time, in us, by a model: rounds of blocks, 4 us and steps of
+// step_us each, and 5 us and the partial sums' way out and back at 5 TB/s where
+// there are any.  (dK and dV of 8 heads of 1000 x 2000 rows at d = 128: 530 us with one
+// block for each tile, two rounds of 148; 487 us with four.)
+int split_simt(long long blocks, long long steps, long long slots, double step_us, double out_bytes) {
+    int best = 1;
+    double least = 0.0;
+    for (long long s = 1; s <= std::min(steps, 64LL); ++s) {
+        double cost = tiles_of(blocks * s, static_cast<int>(slots)) * (tiles_of(steps, static_cast<int>(s)) * step_us + 4.0);
+        if (s > 1) cost += 5.0 + s * out_bytes * 2.0 / 5.0e6;
+        if (s == 1 || cost < least) {
+            least = cost;
+            best = static_cast<int>(s);
+        }
+    }
+    return best;
+}
+
+// CUDA-core pass, in tiles of 64 rows, or of 16 where that is all there are;
+// two key tiles a step, 16 us (7 us).
 Pass plan_simt(long long problems, long long R, int d, long long tiles) {
     Pass p;
     p.kind = R <= 16 ? Pass::kSimtFew : Pass::kSimt;
-    p.blocks = problems * tiles_of(R, p.kind == Pass::kSimtFew ? 16 : lard::attn::kSimtTile);
-    p.splits = split_to_fill(p.blocks, tiles_of(tiles, 2), simt_slots(d));  // two tiles at a time
+    const bool few = p.kind == Pass::kSimtFew;
+    p.blocks = problems * tiles_of(R, few ? 16 : lard::attn::kSimtTile);
+    p.splits = split_simt(p.blocks, tiles_of(tiles, 2), simt_slots(d), few ? 7.0 : 16.0, 4.0 * problems * R * d);
     return p;
 }
 
@@ -371,7 +392,7 @@ struct Fwd {
     lard_dtype dtype;
     int B, Hq, Hkv, n, d;
     float tau;
-    lard_attn_view q, out;
+    lard_attn_view q, out, rest;  // rest.ptr may be NULL
     float* lse;
     struct Seg {
         lard_attn_view k, v;
@@ -443,6 +464,7 @@ FwdArgs<T> fwd_args(const Fwd& f) {
     FwdArgs<T> g;
     g.q = view<const T>(f.q);
     g.out = view<T>(f.out);
+    g.rest = view<T>(f.rest);
     g.lse = f.lse;
     for (int s = 0; s < 2; ++s) {
         const Fwd::Seg& x = f.seg[s < f.nseg ? s : 0];
@@ -461,6 +483,7 @@ template <typename A, typename T>
 void pass_args(A& a, const Fwd& f, const FwdPlan& p, const Pass& x, int split0, const FwdArgs<T>& g) {
     a.q = g.q;
     a.out = g.out;
+    a.rest = g.rest;
     a.lse = g.lse;
     a.nseg = x.nseg;
     a.PB = x.shared ? 1 : f.B;
@@ -578,6 +601,7 @@ Fwd cross_work(const lard_cross_attn& a, const lard_attn_view* v = nullptr) {
         f.seg[0].k = v[1];
         f.seg[0].v = v[2];
         f.out = v[3];
+        f.rest = v[4];
     }
     return f;
 }
@@ -661,9 +685,14 @@ BwdPlan plan_bwd(const lard_cross_attn& a) {
     const int tile = a.dtype == LARD_DTYPE_FP32 ? lard::attn::kSimtTile : 128;
     p.qblocks = BH * tiles_of(R, tile);
     p.kblocks = BH * tiles_of(a.m, tile);
-    const int slots = a.dtype == LARD_DTYPE_FP32 ? simt_slots(a.d) : kSms;
-    p.qsplits = split_to_fill(p.qblocks, tiles_of(a.m, tile), slots);
-    p.ksplits = split_to_fill(p.kblocks, tiles_of(R, tile), slots);
+    const long long qsteps = tiles_of(a.m, tile), ksteps = tiles_of(R, tile);
+    if (a.dtype == LARD_DTYPE_FP32) {
+        p.qsplits = split_simt(p.qblocks, qsteps, simt_slots(a.d), 12.0, 4.0 * BH * R * a.d);
+        p.ksplits = split_simt(p.kblocks, ksteps, simt_slots(a.d), 16.0, 8.0 * BH * a.m * a.d);
+    } else {
+        p.qsplits = split_to_fill(p.qblocks, qsteps, kSms);
+        p.ksplits = split_to_fill(p.kblocks, ksteps, kSms);
+    }
     if (p.qsplits > 1) {
         p.part_q = static_cast<size_t>(p.qsplits) * BH * R * a.d * 4;
         p.sum_rows += BH * R;
@@ -689,7 +718,7 @@ void take_bwd_workspace(Args& g, const BwdPlan& p, void* ws) {
 
 // Adds the partial sums that a backward call left.
 template <typename T, int D>
-lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], const float* part_q,
+lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[9], const float* part_q,
               const float* part_k, const float* part_v, cudaStream_t stream) {
     using namespace lard::attn;
     if (p.sum_rows == 0) return LARD_OK;
@@ -705,7 +734,7 @@ lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn
 }
 
 template <int D>
-lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[9], void* ws,
                        cudaStream_t stream) {
     using namespace lard::attn;
     TcBwdArgs g;
@@ -714,6 +743,7 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_at
         return LARD_ERR_INVALID_ARG;
     g.q = view<const bf16>(v[0]);
     g.out = view<const bf16>(v[3]);
+    g.rest = view<const bf16>(v[8]);
     g.dout = view<const bf16>(v[4]);
     g.dq = view<bf16>(v[5]);
     g.dk = view<bf16>(v[6]);
@@ -746,7 +776,7 @@ lard_status run_bwd_tc(const lard_cross_attn& a, const BwdPlan& p, const lard_at
 }
 
 template <int D>
-lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[9], void* ws,
                          cudaStream_t stream) {
     using namespace lard::attn;
     SimtBwdArgs g;
@@ -775,7 +805,7 @@ lard_status run_bwd_simt(const lard_cross_attn& a, const BwdPlan& p, const lard_
     return st == LARD_OK ? run_sums<float, D>(a, p, v, g.part_q, g.part_k, g.part_v, stream) : st;
 }
 
-lard_status launch_bwd(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[8], void* ws,
+lard_status launch_bwd(const lard_cross_attn& a, const BwdPlan& p, const lard_attn_view (&v)[9], void* ws,
                        cudaStream_t stream) {
     if (a.dtype == LARD_DTYPE_BF16)
         return a.d == 64 ? run_bwd_tc<64>(a, p, v, ws, stream) : run_bwd_tc<128>(a, p, v, ws, stream);
@@ -805,11 +835,13 @@ lard_status lard_cross_attn_fwd(const lard_cross_attn* a, void* workspace, size_
     if (st != LARD_OK) return st;
     const int e = elem_bytes(a->dtype);
     Buffers bufs;
-    lard_attn_view v[4];
+    lard_attn_view v[5] = {};
+    const bool rest = a->dtype == LARD_DTYPE_BF16 && a->rest.ptr;
     if (!bufs.add_view(a->q, a->B, a->Hq, a->n, a->d, e, false, &v[0]) ||
         !bufs.add_view(a->k, a->B, a->Hkv, a->m, a->d, e, false, &v[1]) ||
         !bufs.add_view(a->v, a->B, a->Hkv, a->m, a->d, e, false, &v[2]) ||
-        !bufs.add_view(a->out, a->B, a->Hq, a->n, a->d, e, true, &v[3]))
+        !bufs.add_view(a->out, a->B, a->Hq, a->n, a->d, e, true, &v[3]) ||
+        (rest && !bufs.add_view(a->rest, a->B, a->Hq, a->n, a->d, e, true, &v[4])))
         return LARD_ERR_INVALID_ARG;
     if (!a->lse || !aligned(a->lse, 4) || (a->k_len && !aligned(a->k_len, 4))) return LARD_ERR_INVALID_ARG;
     const Fwd work = cross_work(*a, v);
@@ -833,7 +865,8 @@ lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_
     if (st != LARD_OK) return st;
     const int e = elem_bytes(a->dtype);
     Buffers bufs;
-    lard_attn_view v[8];
+    lard_attn_view v[9] = {};
+    const bool rest = a->dtype == LARD_DTYPE_BF16 && a->rest.ptr;
     if (!bufs.add_view(a->q, a->B, a->Hq, a->n, a->d, e, false, &v[0]) ||
         !bufs.add_view(a->k, a->B, a->Hkv, a->m, a->d, e, false, &v[1]) ||
         !bufs.add_view(a->v, a->B, a->Hkv, a->m, a->d, e, false, &v[2]) ||
@@ -841,7 +874,8 @@ lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspace, size_
         !bufs.add_view(a->dout, a->B, a->Hq, a->n, a->d, e, false, &v[4]) ||
         !bufs.add_view(a->dq, a->B, a->Hq, a->n, a->d, e, true, &v[5]) ||
         !bufs.add_view(a->dk, a->B, a->Hkv, a->m, a->d, e, true, &v[6]) ||
-        !bufs.add_view(a->dv, a->B, a->Hkv, a->m, a->d, e, true, &v[7]))
+        !bufs.add_view(a->dv, a->B, a->Hkv, a->m, a->d, e, true, &v[7]) ||
+        (rest && !bufs.add_view(a->rest, a->B, a->Hq, a->n, a->d, e, false, &v[8])))
         return LARD_ERR_INVALID_ARG;
     if (!a->lse || !aligned(a->lse, 4) || (a->k_len && !aligned(a->k_len, 4))) return LARD_ERR_INVALID_ARG;
     const BwdPlan plan = plan_bwd(*a);

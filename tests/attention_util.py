@@ -14,6 +14,7 @@ in fp32 (one ulp an addition: the tensor cores may truncate).
 * dV: the same with P's columns, E also holding the LSE's own error; and a(rows).
 * dZ = P (dP - delta): dP in fp32 is off by a(d) sum |dO v|; delta by sum_c |dO_c| e_O,c
   (it is formed from the rounded O) + a(d) sum |dO O|; dZ is rounded to the type.
+  With the rest of out's rounding beside it (off by u^2 |O| at most), the u |O| of e_O goes.
 * dQ, dK: tau sum |e_dZ| |k| (|q|), + a(terms) tau sum |dZ k|, + u |dQ|.
 A normal result cannot be below the type's smallest normal, so 1e-30 is added to every
 bound.
@@ -47,9 +48,11 @@ class Row:
         lse0 = torch.where(self.any, self.lse, torch.zeros_like(lse)).abs()
         self.e_lse = top + a(keys) + 2.0 ** -20 + 2.0 ** -22 * lse0
         self.E = 2 * top + a(keys) + 2.0 ** -19
-        self.e_out = ((self.u + self.E)[:, None] * (self.p @ v.abs()) + self.u * self.out.abs() + 1e-30)
+        in_sum = (self.u + self.E)[:, None] * (self.p @ v.abs())
+        self.e_out = in_sum + self.u * self.out.abs() + 1e-30
+        self.e_with_rest = in_sum + self.u ** 2 * self.out.abs() + 2.0 ** -23 * self.out.abs() + 1e-30
 
-    def backward(self, do):
+    def backward(self, do, rest=False):
         """dq, and this head's part of dk, dv, with bounds."""
         d, n, keys, u, tau = self.q.shape[1], self.q.shape[0], self.k.shape[0], self.u, self.tau
         E = (self.E + 2 * self.e_lse)[:, None]
@@ -57,7 +60,7 @@ class Row:
         delta = (do * self.out).sum(-1, keepdim=True)
         dz = self.p * (dp - delta)
         e_dp = a(d) * (do.abs() @ self.v.abs().T)
-        e_delta = ((do.abs() * self.e_out).sum(-1) + a(d) * (do * self.out).abs().sum(-1))[:, None]
+        e_delta = ((do.abs() * (self.e_with_rest if rest else self.e_out)).sum(-1) + a(d) * (do * self.out).abs().sum(-1))[:, None]
         e_dz = (1 + u) * self.p * (1 + E) * (e_dp + e_delta) + (u + E) * dz.abs() + a(2) * self.p * (dp.abs() + delta.abs())
         dq = tau * (dz @ self.k)
         e_dq = tau * (e_dz @ self.k.abs()) + a(keys) * tau * (dz.abs() @ self.k.abs())
@@ -76,8 +79,9 @@ def clamp_len(x, cap):
     return max(0, min(cap, int(x)))
 
 
-def cross(q, k, v, tau, k_len=None, dout=None):
-    """Reference of cross attention: {name: (value, bound)} in float64 on the CPU."""
+def cross(q, k, v, tau, k_len=None, dout=None, rest=False):
+    """Reference of cross attention: {name: (value, bound)} in float64 on the CPU; with rest,
+    "sum" is what out + rest has to be and delta is formed from that."""
     (B, Hq, n, d), (Hkv, m), dt = q.shape, k.shape[1:3], q.dtype
     q, k, v = f64(q), f64(k), f64(v)
     got = {"out": torch.zeros((2, B, Hq, n, d), dtype=torch.float64), "lse": torch.zeros((2, B, Hq, n), dtype=torch.float64)}
@@ -85,6 +89,8 @@ def cross(q, k, v, tau, k_len=None, dout=None):
         dout = f64(dout)
         got["dq"] = torch.zeros((2, B, Hq, n, d), dtype=torch.float64)
         got["dk"], got["dv"] = (torch.zeros((2, B, Hkv, m, d), dtype=torch.float64) for _ in range(2))
+    if rest:
+        got["sum"] = torch.zeros((2, B, Hq, n, d), dtype=torch.float64)
     for b in range(B):
         size = m if k_len is None else clamp_len(k_len[b], m)
         for h in range(Hq):
@@ -92,8 +98,10 @@ def cross(q, k, v, tau, k_len=None, dout=None):
             r = Row(q[b, h], k[b, g, :size], v[b, g, :size], torch.ones((n, size), dtype=torch.bool), tau, dt)
             got["out"][0, b, h], got["out"][1, b, h] = r.out, r.e_out
             got["lse"][0, b, h], got["lse"][1, b, h] = r.lse, r.e_lse
+            if rest:
+                got["sum"][0, b, h], got["sum"][1, b, h] = r.out, r.e_with_rest
             if dout is not None:
-                dq, dk, dv = r.backward(dout[b, h])
+                dq, dk, dv = r.backward(dout[b, h], rest)
                 got["dq"][0, b, h], got["dq"][1, b, h] = dq
                 for name, x in (("dk", dk), ("dv", dv)):
                     got[name][0, b, g, :size] += x[0]

@@ -21,7 +21,7 @@ class View(ctypes.Structure):
 class Cross(ctypes.Structure):
     _fields_ = ([(x, ctypes.c_int) for x in ("dtype", "B", "Hq", "Hkv", "n", "m", "d")] + [("tau", ctypes.c_float)] +
                 [(x, View) for x in "qkv"] + [("k_len", ctypes.c_void_p), ("out", View), ("lse", ctypes.c_void_p)] +
-                [(x, View) for x in ("dout", "dq", "dk", "dv")])
+                [(x, View) for x in ("dout", "dq", "dk", "dv", "rest")])
 
 
 class Prefix(ctypes.Structure):
@@ -48,9 +48,9 @@ def test_exports_match_the_header(att):
 
 def test_packed_arguments_have_the_structs_layout(att):
     assert att._CROSS.size == ctypes.sizeof(Cross) and att._PREFIX.size == ctypes.sizeof(Prefix)
-    c = Cross.from_buffer_copy(att._CROSS.pack(*range(7), 0.5, *range(8, 42)))
-    assert (c.d, c.tau, c.q.ptr, c.k.ptr, c.v.row, c.k_len, c.out.ptr, c.lse, c.dout.ptr, c.dv.row) == (
-        6, 0.5, 8, 12, 19, 20, 21, 25, 26, 41)
+    c = Cross.from_buffer_copy(att._CROSS.pack(*range(7), 0.5, *range(8, 46)))
+    assert (c.d, c.tau, c.q.ptr, c.k.ptr, c.v.row, c.k_len, c.out.ptr, c.lse, c.dout.ptr, c.dv.row, c.rest.ptr) == (
+        6, 0.5, 8, 12, 19, 20, 21, 25, 26, 41, 42)
     p = Prefix.from_buffer_copy(att._PREFIX.pack(*range(8), 0.5, *range(9, 35)))
     assert (p.d, p.tau, p.q.ptr, p.kp.ptr, p.vs.row, p.s_len, p.out.ptr, p.lse) == (7, 0.5, 9, 13, 28, 29, 30, 34)
 
@@ -87,6 +87,11 @@ def test_valid_arguments_reach_the_device_check(att):
     assert cross_call(att) == end and cross_call(att, "bwd") == end and prefix_call(att) == end
     assert prefix_call(att, P=100000) == end
     assert cross_call(att, k_batch=0, v_head=0) == end                 # inputs may be shared
+    rest = dict(rest_ptr=9 * STEP, rest_batch=4 * 50 * 64, rest_head=50 * 64, rest_row=64)
+    assert cross_call(att, **rest) == end and cross_call(att, "bwd", **rest) == end
+    assert cross_call(att, **dict(rest, rest_ptr=4 * STEP)) == 1 and cross_call(att, **dict(rest, rest_row=63)) == 1
+    assert cross_call(att, "bwd", **dict(rest, rest_ptr=6 * STEP)) == 1     # an input of the backward pass, over dq
+    assert cross_call(att, dtype=1, **dict(rest, rest_ptr=4 * STEP)) == end  # not used for fp32
     assert cross_call(att, B=1, q_batch=7, out_batch=3) == end         # the stride of one element is not used
     assert prefix_call(att, P=0, kp_ptr=None, vp_ptr=None) == end
     assert prefix_call(att, S=0, ks_ptr=None, vs_ptr=None, s_len=1) == end

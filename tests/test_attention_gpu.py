@@ -132,6 +132,26 @@ def test_gradients_of_long_and_narrow_calls(att, n, m, dtype, d):
     au.check(got, au.cross(q, k, v, tau, k_len, do))
 
 
+# One row tile and several, few rows, and both with the key axis split.
+@pytest.mark.parametrize("n,m", [(3, 90), (2, 9000), (30, 200), (40, 4000), (300, 260), (300, 3000)])
+@pytest.mark.parametrize("d", [64, 128])
+def test_rest_of_the_rounding(att, n, m, d):
+    """out + rest is the output to twice the digits, whichever kernel wrote them, and the
+    gradients that take both have no part of out's rounding in delta."""
+    q, k, v, do, tau = cross_inputs(2, 4, 2, n, m, d, BF16, "bnhd", seed=37)
+    k_len = [m, m // 2]
+    got = {x: torch.empty_like(q) for x in ("out", "rest", "dq")} | {x: torch.empty_like(k) for x in ("dk", "dv")}
+    got["lse"] = torch.empty((2, 4, n), device="cuda")
+    ws = torch.empty((max(att.lard_cross_attn_fwd_workspace_bytes(q, k),
+                          att.lard_cross_attn_bwd_workspace_bytes(q, k)),), dtype=torch.uint8, device="cuda")
+    att.lard_cross_attn_fwd(q, k, v, tau, got["out"], got["lse"], lens(k_len), ws, rest=got["rest"])
+    att.lard_cross_attn_bwd(q, k, v, tau, got["out"], got["lse"], do, got["dq"], got["dk"], got["dv"], lens(k_len), ws,
+                            rest=got["rest"])
+    att.lard_attn_device_status()
+    got["sum"] = got["out"].double() + got["rest"].double()
+    au.check(got, au.cross(q, k, v, tau, k_len, do, rest=True))
+
+
 def test_large_and_rising_logits(att):
     """Row maxima that rise tile after tile by far, and logits of several hundreds."""
     for dtype in (BF16, FP32):
