@@ -116,7 +116,7 @@ LARD_API lard_status lard_cross_attn_bwd(const lard_cross_attn* a, void* workspa
  *               Query i sees every shared row and its sequence's own rows
  *               j <= s_len - n + i (none where that is negative).
  *   out     out [B, Hq, n, d];  lse out [B, Hq, n].
- * A non-finite value in an own row reaches every new row of that sequence.
+ * A non-finite value in an own row may reach every new row of that sequence.
  * Deterministic.  There is no backward pass (a serving operator).
  */
 typedef struct lard_prefix_attn_args {

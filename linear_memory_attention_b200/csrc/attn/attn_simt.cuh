@@ -519,8 +519,9 @@ __global__ void __launch_bounds__(kSimtThreads) attn_dkdv_simt_kernel(const __gr
         const size_t prow = ((static_cast<size_t>(split) * g.B * g.Hkv + bh) * g.m + j) * D;
         float* dst = part ? (grp ? g.part_k : g.part_v) + prow : (grp ? g.dk : g.dv).row(b, hk, j);
 #pragma unroll
-        for (int u = 0; u < D / 64; ++u)
-            store4(dst + 64 * u + 4 * tx, scaled(acc[a][2 * u], acc[a][2 * u + 1], grp && !part ? g.tau : 1.f));
+        for (int u = 0; u < D / 64; ++u)  // zeros past the length, whatever dO holds
+            store4(dst + 64 * u + 4 * tx, j < len ? scaled(acc[a][2 * u], acc[a][2 * u + 1], grp && !part ? g.tau : 1.f)
+                                                  : make_float4(0.f, 0.f, 0.f, 0.f));
     }
 }
 

@@ -103,6 +103,43 @@ def test_padding_may_hold_anything(att, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n,m", [(40, 150), (4, 2000)])
+def test_gradient_rows_past_the_length_are_zeros(att, n, m, dtype):
+    """Also where the upstream gradient holds infinities and NaN."""
+    q, k, v, do, tau = cross_inputs(2, 4, 2, n, m, 64, dtype, seed=15)
+    k_len = [70, 0]
+    do[:, :, 0] = float("inf")
+    do[:, :, n - 1] = float("nan")
+    got = att.cross_attention(q, k, v, tau, lens(k_len), dout=do)
+    for b, size in enumerate(k_len):
+        assert not got["dk"][b, :, size:].any() and not got["dv"][b, :, size:].any()
+    assert not got["dq"][1].any() and not got["out"][1].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("n", [130, 16])
+def test_offsets_past_32_bits(att, n, dtype):
+    """Rows, heads and tensors of one buffer of more than 2^31 elements, eight views interleaved."""
+    B, H, d, step = 1, 2, 64, 1 << 24
+    big = torch.empty(((n if n > 128 else 130) * step,), dtype=dtype, device="cuda")
+    row = step if n > 128 else 2 * d * 8
+    head = d * 8 if n > 128 else 1 << 31
+    at = {}
+    for x, name in enumerate(("q", "k", "v", "do", "out", "dq", "dk", "dv")):
+        at[name] = big.as_strided((B, H, n, d), (0, head, row, 1), x * d)
+        at[name].copy_(au.randn((B, H, n, d), dtype, 170 + x))
+    q, k, v, do, tau = at["q"], at["k"], at["v"], at["do"], 1.0 / math.sqrt(d)
+    want = au.cross(q, k, v, tau, None, do)
+    at["lse"] = torch.empty((B, H, n), device="cuda")
+    ws = torch.empty((max(att.lard_cross_attn_fwd_workspace_bytes(q, k),
+                          att.lard_cross_attn_bwd_workspace_bytes(q, k), 16),), dtype=torch.uint8, device="cuda")
+    att.lard_cross_attn_fwd(q, k, v, tau, at["out"], at["lse"], None, ws)
+    att.lard_cross_attn_bwd(q, k, v, tau, at["out"], at["lse"], do, at["dq"], at["dk"], at["dv"], None, ws)
+    att.lard_attn_device_status()
+    au.check(at, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_shared_keys(att, dtype):
     """One key block for all sequences (batch stride 0) and for all heads (head stride 0)."""
     q, k, v, _, tau = cross_inputs(3, 4, 2, 33, 90, 64, dtype, seed=21)
