@@ -276,9 +276,6 @@ struct FwdPlan {
     }
 };
 
-// Blocks that run at once: one an SM at d = 128, two at d = 64 (shared memory).
-int simt_slots(int d) { return d == 64 ? 2 * kSms : kSms; }
-
 // How many blocks share a long axis of `steps` tiles when there are `blocks`
 // without: as many as fill the GPU once, where one set would leave it partly idle.
 int split_to_fill(long long blocks, long long steps, long long slots) {
@@ -287,8 +284,8 @@ int split_to_fill(long long blocks, long long steps, long long slots) {
 }
 
 // The same for the CUDA-core kernels, whose blocks are few and long: the number
-// with the least time, in us, by a model: rounds of blocks, 4 us and steps of
-// step_us each, and 5 us and the partial sums' way out and back at 5 TB/s where
+// with the least time, in us, by a model: rounds of blocks (one an SM: their
+// registers, or at 16 rows their shared memory), 4 us and steps of step_us each, and 5 us and the partial sums' way out and back at 5 TB/s where
 // there are any.  (dK and dV of 8 heads of 1000 x 2000 rows at d = 128: 530 us with one
 // block for each tile, two rounds of 148; 487 us with four.)
 int split_simt(long long blocks, long long steps, long long slots, double step_us, double out_bytes) {
@@ -312,7 +309,7 @@ Pass plan_simt(long long problems, long long R, int d, long long tiles) {
     p.kind = R <= 16 ? Pass::kSimtFew : Pass::kSimt;
     const bool few = p.kind == Pass::kSimtFew;
     p.blocks = problems * tiles_of(R, few ? 16 : lard::attn::kSimtTile);
-    p.splits = split_simt(p.blocks, tiles_of(tiles, 2), simt_slots(d), few ? 7.0 : 16.0, 4.0 * problems * R * d);
+    p.splits = split_simt(p.blocks, tiles_of(tiles, 2), kSms, few ? 7.0 : 16.0, 4.0 * problems * R * d);
     return p;
 }
 
@@ -687,8 +684,8 @@ BwdPlan plan_bwd(const lard_cross_attn& a) {
     p.kblocks = BH * tiles_of(a.m, tile);
     const long long qsteps = tiles_of(a.m, tile), ksteps = tiles_of(R, tile);
     if (a.dtype == LARD_DTYPE_FP32) {
-        p.qsplits = split_simt(p.qblocks, qsteps, simt_slots(a.d), 12.0, 4.0 * BH * R * a.d);
-        p.ksplits = split_simt(p.kblocks, ksteps, simt_slots(a.d), 16.0, 8.0 * BH * a.m * a.d);
+        p.qsplits = split_simt(p.qblocks, qsteps, kSms, 12.0, 4.0 * BH * R * a.d);
+        p.ksplits = split_simt(p.kblocks, ksteps, kSms, 16.0, 8.0 * BH * a.m * a.d);
     } else {
         p.qsplits = split_to_fill(p.qblocks, qsteps, kSms);
         p.ksplits = split_to_fill(p.kblocks, ksteps, kSms);
