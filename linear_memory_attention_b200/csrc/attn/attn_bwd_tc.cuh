@@ -22,6 +22,11 @@
 //   TMEM: dV [0, D), dK [128, 128 + D), S^T of unit u at 256 + 64 (u & 1), dP^T at 384 + 64 (u & 1).
 // Per 128 x 128 tile at d = 128 (tensor pipe / shared memory, cycles): dQ 1536 / 1536;
 // dK, dV 2048 / 2816, since a 64-row unit reads the resident K and V once each.
+// Measured, 4096 rows x 8000 keys, 32 heads, d = 128: dQ 682 us (1.18 PFLOP/s), dK and dV
+// 935 us (1.15 PFLOP/s); the tensor pipe is busy 79 % of the time in either, and what
+// is left is the chain from a product's end to the next one's operands.
+// Few blocks (one long axis): the other axis is split so that the SMs are filled once, and
+// the partial sums are added in order (attn_join.cuh).
 #pragma once
 
 #include "attn_common.cuh"

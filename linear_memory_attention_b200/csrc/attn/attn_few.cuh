@@ -2,7 +2,10 @@
 // single tokens of grouped heads, short queries.
 //
 // Such a pass reads every key and value for a few multiply-adds: HBM bounds it,
-// and what counts is bytes in flight.  Each warp takes groups of 16 keys on its
+// and what counts is bytes in flight (three blocks an SM, 64 KB of boxes each).
+// Measured, 16 sequences x 8 key heads x 8000 keys at d = 128 (524 MB where all are
+// used): 84 us, 6.2 TB/s; of ragged lengths, 378 MB, 72 us, 5.2 TB/s: the longest
+// sequences' blocks end last.  Each warp takes groups of 16 keys on its
 // own, which TMA brings into a queue of its own in shared memory (boxes of 16
 // rows x 64 columns, 128-byte swizzle), and feeds them to m16n8k16 products;
 // warps never wait for one another until the end.  The order of a product's
@@ -14,7 +17,8 @@
 //   O += P V    inner index key: S's accumulators are P's A fragments as they are.
 //               Output column n of product t stands for d = 64 (t / 8) + 8 n + t % 8,
 //               so that a lane takes piece g of its four keys' chunks.
-// (Single rows by untiled bulk copies stop at one copy per 16 cycles and SM.)
+// (Single rows by untiled bulk copies stop at one copy per 16 cycles and SM; they and
+// 16-byte copies by the threads reach 4.1 to 4.3 TB/s.)
 // Rows' maxima, sums and O are per warp; a reference m rises only by steps above
 // 2^8, as in the tensor-core pass.  The warps of a block are joined through
 // shared memory, the blocks of a cluster (up to 8 share a problem's keys)

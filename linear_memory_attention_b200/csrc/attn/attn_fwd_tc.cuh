@@ -13,9 +13,19 @@
 // A row's reference m follows its maximum only when that has risen by more
 // than 2^8: P then stays below 2^8 and in bf16's relative precision whatever
 // m is, O and l are rescaled rarely, and the softmax threads do it themselves.
-// Per tile the tensor pipe needs 1024 cycles at d = 128 and the exponential
-// unit 1024 (128 * 128 / 16): both are near their limit, so a share of the
-// exponentials is computed on the FMA pipe.
+// What bounds it: a stream's chain of S, exponentials, P V per tile, of which two
+// streams overlap.  At d = 128 a tile's products take 1024 cycles of the tensor pipe
+// and its exponentials 1024 (128 x 128 / 16) of their unit; a step (a tile of each
+// stream) takes about 3650: 1450 from a stream's P to its next S (products of both
+// streams and some 340 cycles from the last product to who waits for it), 2100 for
+// its softmax.  Measured, one B200: 4096 rows x 16384 keys, 32 heads over 8, d = 128: 0.88 ms
+// and 52 us of joining, 1.25 PFLOP/s (alternated with other work; under the
+// 1000 W cap 1.02 ms); 4 x 4096 x 4096, d = 64: 765 us, 718 TFLOP/s, where the
+// exponential unit is the nearer bound (tiles of 64 keys and two blocks an SM: 20 %
+// over tiles of 128 and one).
+// Tried and slower at d = 128: four softmax warpgroups; part of the exponentials on
+// the FMA pipe; units of 64 keys with two S a stream (1.25 ms); one stream a block
+// and two blocks an SM (10 %).
 // Key tiles past a sequence's length are never visited.  Values of rows past
 // it inside the last tile are zeroed in shared memory before the product (0
 // times what is there could be NaN); their logits are replaced by -infinity.
