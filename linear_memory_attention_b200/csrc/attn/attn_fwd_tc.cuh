@@ -19,7 +19,7 @@
 // stream) takes about 3650: 1450 from a stream's P to its next S (products of both
 // streams and some 340 cycles from the last product to who waits for it), 2100 for
 // its softmax.  Measured, one B200: 4096 rows x 16384 keys, 32 heads over 8, d = 128: 0.88 ms
-// and 52 us of joining, 1.25 PFLOP/s (alternated with other work; under the
+// and 47 us of joining, 1.25 PFLOP/s (alternated with other work; under the
 // 1000 W cap 1.02 ms); 4 x 4096 x 4096, d = 64: 765 us, 718 TFLOP/s, where the
 // exponential unit is the nearer bound (tiles of 64 keys and two blocks an SM: 20 %
 // over tiles of 128 and one).

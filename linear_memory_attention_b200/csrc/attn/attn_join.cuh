@@ -1,7 +1,8 @@
 // attn_join.cuh -- what is left when an axis was split over blocks: joining the
 // forward pass's partial rows, adding the backward pass's partial sums.
 // Both read what the blocks before left in L2 or HBM and are bound by that (131072 rows
-// of two parts at d = 128: 168 MB in and out in 52 us with the launch).
+// of two parts at d = 128: 168 MB in and out in 47 us, while HBM also takes what L2 could
+// not keep of the parts).
 #pragma once
 
 #include <type_traits>
@@ -35,57 +36,80 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&x)[E
 }
 
 // Joins the splits of a row: LSE = log sum_s exp LSE_s, O = sum_s exp(LSE_s - LSE) O_s.
-// One warp per row; lanes share the splits' weights, then the head dimension.  The
-// parts of four splits are requested at a time, the first before the weights are known.
-template <typename T, int D>
+// A warp has RPW rows (1 or 8): its lanes share the rows' weights, LPR lanes a row, then
+// row by row the head dimension, with the parts of four splits requested at a time.
+// What a row costs beside its bytes (weights, divisions for its address) is then done
+// for eight rows at once: 131072 rows of two parts take 54 us with one row a warp, 47 us
+// with eight.  Few rows are left to a warp each, and the first parts are requested
+// before the weights are known.
+template <typename T, int D, int RPW>
 __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs<T> g) {
     wait_for_kernel_before();
-    const int lane = threadIdx.x & 31;
-    const long long row = (static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    if (row >= g.rows) return;
-    constexpr int E = D / 32, kBatch = 4;
-    const float* part = g.part_o + row * D + lane * E;
-    float x[kBatch][E];
-    auto request = [&](int s) {
+    constexpr int E = D / 32, LPR = 32 / RPW, kBatch = 4;
+    const int lane = threadIdx.x & 31, sub = lane % LPR;
+    const unsigned rows = static_cast<unsigned>(g.rows);  // below 2^31 where there is a join
+    const unsigned row0 = (blockIdx.x * blockDim.x + threadIdx.x) / 32 * RPW, row = row0 + lane / LPR;
+    if (row0 >= rows) return;
+    const bool in = row < rows;
+    const float* part = g.part_o + static_cast<size_t>(row0) * D + lane * E;
+    auto request = [&](float (&x)[kBatch][E], int k, int s) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k)
-            if (s + k < g.splits) load_piece<E>(part + (s + k) * g.rows * D, x[k]);
+        for (int j = 0; j < kBatch; ++j)
+            if (s + j < g.splits && row0 + k < rows) load_piece<E>(part + ((s + j) * g.rows + k) * D, x[j]);
     };
-    request(0);
-    float top = -INFINITY;
-    for (int s = lane; s < g.splits; s += 32) top = fmaxf(top, g.part_lse[s * g.rows + row]);
+    float first[kBatch][E];
+    if (RPW == 1) request(first, 0, 0);
+    auto lse_of = [&](int s) { return in && s < g.splits ? g.part_lse[s * g.rows + row] : -INFINITY; };
+    float top = -INFINITY, total = 0.f;
+    for (int s = sub; s < g.splits; s += LPR) top = fmaxf(top, lse_of(s));
 #pragma unroll
-    for (int k = 16; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+    for (int k = LPR / 2; k > 0; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
     const float base = top == -INFINITY ? 0.f : top;
-    float total = 0.f, o[E], mine = 0.f;
+    for (int s = sub; s < g.splits; s += LPR) total += exp2f((lse_of(s) - base) * kLog2e);
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    for (int s = 0; s < g.splits; s += kBatch) {
-        if (s > 0) request(s);
-        if (s % 32 == 0) mine = s + lane < g.splits ? exp2f((g.part_lse[(s + lane) * g.rows + row] - base) * kLog2e) : 0.f;
+    for (int k = LPR / 2; k > 0; k >>= 1) total += __shfl_xor_sync(0xffffffffu, total, k);
+    const float inv = total == 0.f ? 0.f : 1.f / total;
+
+    float o[RPW][E];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) {
-            const float w = __shfl_sync(0xffffffffu, mine, (s + k) % 32);
-            if (s + k >= g.splits) continue;
-            total += w;
+    for (int k = 0; k < RPW; ++k)
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = w == 0.f ? o[e] : fmaf(w, x[k][e], o[e]);
+        for (int e = 0; e < E; ++e) o[k][e] = 0.f;
+    for (int s0 = 0; s0 < g.splits; s0 += LPR) {
+        const float mine = exp2f((lse_of(s0 + sub) - base) * kLog2e) * inv;
+        for (int j0 = 0; j0 < LPR && s0 + j0 < g.splits; j0 += kBatch) {
+#pragma unroll
+            for (int k = 0; k < RPW; ++k) {
+                float x[kBatch][E];
+                if (RPW > 1 || s0 + j0 > 0) request(x, k, s0 + j0);
+#pragma unroll
+                for (int j = 0; j < kBatch; ++j) {
+                    const float w = __shfl_sync(0xffffffffu, mine, k * LPR + j0 + j);
+                    if (w == 0.f) continue;  // nothing seen, or no such split
+#pragma unroll
+                    for (int e = 0; e < E; ++e) o[k][e] = fmaf(w, RPW == 1 && s0 + j0 == 0 ? first[j][e] : x[j][e], o[k][e]);
+                }
+            }
         }
     }
-    const float inv = total == 0.f ? 0.f : 1.f / total;
-    const int R = g.G * g.n;
-    const int bh = static_cast<int>(row / R), r = static_cast<int>(row % R);
+    const unsigned R = static_cast<unsigned>(g.G) * g.n, at = in ? row : 0;
+    const int bh = static_cast<int>(at / R), r = static_cast<int>(at % R);
     const int b = bh / g.Hkv, head = bh % g.Hkv * g.G + r / g.n, pos = r % g.n;
+    T* out = g.out.row(b, head, pos);
+    T* rest = g.rest.p ? g.rest.row(b, head, pos) : nullptr;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= inv;
-    store_piece<E>(g.out.row(b, head, pos) + lane * E, o);
-    if constexpr (std::is_same<T, __nv_bfloat16>::value)
-        if (g.rest.p) {
+    for (int k = 0; k < RPW; ++k) {
+        T* dst = shfl_ptr(out, k * LPR);
+        if (row0 + k < rows) store_piece<E>(dst + lane * E, o[k]);
+        if constexpr (std::is_same<T, __nv_bfloat16>::value)
+            if (g.rest.p) {
+                dst = shfl_ptr(rest, k * LPR);
 #pragma unroll
-            for (int e = 0; e < E; ++e) o[e] = rounding_rest(o[e]);
-            store_piece<E>(g.rest.row(b, head, pos) + lane * E, o);
-        }
-    if (lane == 0) g.lse[row] = total == 0.f ? -INFINITY : base + log2f(total) * kLn2;
+                for (int e = 0; e < E; ++e) o[k][e] = rounding_rest(o[k][e]);
+                if (row0 + k < rows) store_piece<E>(dst + lane * E, o[k]);
+            }
+    }
+    if (in && sub == 0) g.lse[row] = total == 0.f ? -INFINITY : base + log2f(total) * kLn2;
 }
 
 // Sums of up to three gradients: dst row = scale * sum_s src[s][row], s in order.

@@ -242,7 +242,10 @@ lard_status launch(void (*kernel)(Params...), long long grid, int threads, int s
 }
 
 // ------------------------------------------------------------------ forward
-constexpr long long kJoinRowsPerBlock = 8;
+constexpr long long kSumRowsPerBlock = 8;
+// Rows from which a join's warp takes eight (one row: 5.6 us for 4096 rows of eight parts,
+// 7.3 for 8192 of four, 10.5 for 16384 of two; eight: 9.9, 7.3 and 7.2 us).
+constexpr long long kManyRows = 8192;
 
 long long tiles_of(long long rows, int tile) { return (rows + tile - 1) / tile; }
 
@@ -272,7 +275,7 @@ struct FwdPlan {
     bool grids_fit() const {
         for (int k = 0; k < npass; ++k)
             if (pass[k].blocks * pass[k].splits > INT_MAX) return false;
-        return tiles_of(rows, kJoinRowsPerBlock) <= INT_MAX;
+        return !join() || rows <= INT_MAX;
     }
 };
 
@@ -577,7 +580,9 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
         if (st != LARD_OK) return st;
         split0 += x.splits;
     }
-    return p.join() ? launch(attn_join_kernel<T, D>, tiles_of(p.rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, g) : LARD_OK;
+    if (!p.join()) return LARD_OK;
+    return p.rows >= kManyRows ? launch(attn_join_kernel<T, D, 8>, tiles_of(p.rows, 64), 256, 0, stream, true, 0, g)
+                               : launch(attn_join_kernel<T, D, 1>, tiles_of(p.rows, 8), 256, 0, stream, true, 0, g);
 }
 
 Fwd cross_work(const lard_cross_attn& a, const lard_attn_view* v = nullptr) {
@@ -671,7 +676,7 @@ struct BwdPlan {
     long long sum_rows = 0;
     size_t bytes() const { return delta + part_q + 2 * part_kv; }
     bool grids_fit() const {
-        return qblocks * qsplits <= INT_MAX && kblocks * ksplits <= INT_MAX && tiles_of(sum_rows, kJoinRowsPerBlock) <= INT_MAX;
+        return qblocks * qsplits <= INT_MAX && kblocks * ksplits <= INT_MAX && tiles_of(sum_rows, kSumRowsPerBlock) <= INT_MAX;
     }
 };
 
@@ -727,7 +732,7 @@ lard_status run_sums(const lard_cross_attn& a, const BwdPlan& p, const lard_attn
         s.job[s.jobs++] = {part_k, view<T>(v[6]), p.ksplits, a.Hkv, a.m, static_cast<long long>(a.B) * a.Hkv * a.m, a.tau};
         s.job[s.jobs++] = {part_v, view<T>(v[7]), p.ksplits, a.Hkv, a.m, static_cast<long long>(a.B) * a.Hkv * a.m, 1.f};
     }
-    return launch(attn_sum_kernel<T, D>, tiles_of(p.sum_rows, kJoinRowsPerBlock), 256, 0, stream, true, 0, s);
+    return launch(attn_sum_kernel<T, D>, tiles_of(p.sum_rows, kSumRowsPerBlock), 256, 0, stream, true, 0, s);
 }
 
 template <int D>
