@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             stats[256 * i + row] = m;
             stats[256 * i + 128 + row] = l;
             if (ok && mine > 0) {
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < D / 2; c += 32) {
                     const int col = (1 - i) * (D / 2) + c;
                     float o[32];
@@ -483,37 +483,38 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             constexpr int kCols = kByKeys ? D / 2 : D, kPart = kByKeys ? D / 4 : 32;
             const int col0 = kByKeys ? i * (D / 2) : 0;
             const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? (4 * i + q4) * (L::TILE / 8) : i * L::TILE + q4 * (L::TILE / 4));
-            auto write = [&](bool rest) {
+            // Loops that are not unrolled: short calls wait for instructions here.
+#pragma unroll 1
+            for (int pass = 0; pass < (g.rest.p && !g.join ? 2 : 1); ++pass) {
+                const bool rest = pass == 1;
+#pragma unroll 1
+                for (int c = 0; c < kCols; c += 32) {
+                    float o[32];
+                    __syncwarp();
+                    if (mine > 0) {
+                        ptx::tmem_ld32(to + col0 + c, o);
+                        ptx::tmem_ld_wait(o);
 #pragma unroll
-            for (int c = 0; c < kCols; c += 32) {
-                float o[32];
-                __syncwarp();
-                if (mine > 0) {
-                    ptx::tmem_ld32(to + col0 + c, o);
-                    ptx::tmem_ld_wait(o);
+                        for (int k = 0; k < 32; ++k) o[k] *= w0;
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] *= w0;
-                } else {
+                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                    }
+                    if (other) {
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = 0.f;
+                        for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(col0 + c + k) * 128 + row], w1, o[k]);
+                    }
+                    if (rest) {
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] = rounding_rest(o[k]);
+                    }
+                    if (g.join)
+                        fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + col0 + c : nullptr);
+                    else
+                        stage_bf16<kCols * 2>(area, lane, c / 8, o, 1.f);
                 }
-                if (other) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(col0 + c + k) * 128 + row], w1, o[k]);
-                }
-                if (rest) {
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = rounding_rest(o[k]);
-                }
-                if (g.join)
-                    fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + col0 + c : nullptr);
-                else
-                    stage_bf16<kCols * 2>(area, lane, c / 8, o, 1.f);
+                if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? (rest ? g.rest : g.out).row(b, head, pos) + col0 : nullptr, lane);
             }
-            if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? (rest ? g.rest : g.out).row(b, head, pos) + col0 : nullptr, lane);
-            };
-            write(false);
-            if (g.rest.p && !g.join) write(true);
             if (row_ok && (!kByKeys || i == 0)) {
                 if (g.join) g.part_lse[prow] = lse;
                 else g.lse[grow] = lse;
