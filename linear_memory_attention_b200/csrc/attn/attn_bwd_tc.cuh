@@ -23,8 +23,8 @@
 // Per 128 x 128 tile at d = 128 (tensor pipe / shared memory, cycles): dQ 1536 / 1536;
 // dK, dV 2048 / 2816, since a 64-row unit reads the resident K and V once each.
 // Measured, 4096 rows x 8000 keys, 32 heads, d = 128: dQ 682 us (1.18 PFLOP/s), dK and dV
-// 935 us (1.15 PFLOP/s); the tensor pipe is busy 79 % of the time in either, and what
-// is left is the chain from a product's end to the next one's operands.
+// 935 us (1.15 PFLOP/s) under the 1000 W cap; the tensor pipe is busy 53 to 55 % of the time in
+// either, and what is left is the chain from a product's end to the next one's operands.
 // Few blocks (one long axis): the other axis is split so that the SMs are filled once, and
 // the partial sums are added in order (attn_join.cuh).
 #pragma once

@@ -8,9 +8,9 @@
 // arrive by cp.async meanwhile.  (8 x 4 logits a thread halve the shared-memory
 // traffic and the warps: 10 % slower.  The same 4 x 4 with a warp's threads 4 x 8
 // in place of 2 x 16, two thirds of the traffic: 2 % slower.)
-// Measured, 8 heads of 1000 x 2000 rows at d = 128: 277 us forward (29.6 TFLOP/s), dQ
-// 402 us, dK and dV 487 us; the FMA pipe is busy 58 % of the time on SMs that have
-// a block, of which the forward pass and dQ fill 128 of 148.
+// Measured, 8 heads of 1000 x 2000 rows at d = 128: forward 278 us (29.5 TFLOP/s, the
+// FMA pipe busy 51 % of the time, 59 % on the 128 of 148 SMs that have a block), dQ 391 us
+// (52 %), dK and dV 491 us (56 %), their sums 20 us.
 // Forward: the groups take alternate key tiles and are joined at the end; running row
 // maximum and sum in the log2 domain, P through shared memory, O in registers.
 // Backward: one kernel for each side of the logits, so that every sum has one
