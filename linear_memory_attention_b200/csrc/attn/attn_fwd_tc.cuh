@@ -101,7 +101,8 @@ constexpr int kFwdTcThreads = 384;
 
 struct FwdTcCtrl {
     uint64_t kv_full[8], kv_empty[8];
-    uint64_t q_ready, tail_ready, mma_done;
+    uint64_t q_ready, mma_done;
+    uint64_t tail_ready[2];  // of either segment: the producer may be a tail ahead of the issuer
     uint64_t s_full[2], p_full[2], o_full[2];
     uint32_t tmem_base;
     int abort_flag;
@@ -157,9 +158,9 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             ptx::mbar_init(&ctrl->kv_empty[s], 1);
         }
         ptx::mbar_init(&ctrl->q_ready, 8);
-        ptx::mbar_init(&ctrl->tail_ready, 1);
         ptx::mbar_init(&ctrl->mma_done, 1);
         for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(&ctrl->tail_ready[i], 1);
             ptx::mbar_init(&ctrl->s_full[i], 1);
             ptx::mbar_init(&ctrl->p_full[i], 4);
             ptx::mbar_init(&ctrl->o_full[i], 1);
@@ -221,7 +222,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
                             *reinterpret_cast<uint4*>(v + c * KT * 128 + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                     ptx::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ptx::mbar_arrive(&ctrl->tail_ready);
+                    if (lane == 0) ptx::mbar_arrive(&ctrl->tail_ready[seg_of(tile)]);
                 }
                 if (++slot == L::NS) { slot = 0; ++round; }
             }
@@ -290,7 +291,6 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
                 issue_s(i, k[i]);
                 if (kByKeys || i == nstream - 1) release(k[i]);
             }
-            int tails = 0;
             for (int t = 0; ok && t < S; ++t) {
                 const bool both = t < steps1;                  // stream 1 takes part in this step,
                 const bool more0 = t + 1 < S, more1 = t + 1 < steps1;  // and either in the next
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
                     if (kByKeys || i == 0) {
                         ok = ok && wait_place(v[i]);
                         // Rows past a sequence's end: the producer makes them zeros.
-                        if (ok && is_tail(tile_of(t, i))) ok = wait(&ctrl->tail_ready, tails++ & 1);
+                        if (ok && is_tail(tile_of(t, i))) ok = wait(&ctrl->tail_ready[seg_of(tile_of(t, i))], 0);
                     }
                     ok = ok && wait(&ctrl->p_full[i], t & 1);
                     if (!ok) break;

@@ -233,6 +233,23 @@ def test_prefix_attention(att, case, dtype, d):
     au.check(got, au.prefix(q, kp, vp, ks, vs, s_len, tau))
 
 
+# One sequence takes shared and own rows in one pass: both may end inside a tile.
+ONE = [(1, 4, 2, 3, 239, 60), (1, 2, 1, 40, 15, 2), (1, 4, 2, 67, 2, 99), (1, 2, 2, 5, 242, 9),
+       (1, 2, 1, 174, 8, 12), (1, 2, 2, 19, 754, 118), (1, 2, 1, 300, 2000, 301), (1, 16, 1, 1, 1000, 31)]
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("case", ONE, ids=lambda c: "x".join(map(str, c)))
+def test_prefix_of_one_sequence(att, case, dtype, d):
+    B, Hq, Hkv, n, P, S = case
+    for s_len in (None, [S // 2]):
+        q, kp, vp, ks, vs, tau = prefix_inputs(B, Hq, Hkv, n, P, S, d, dtype, seed=d + n)
+        got = att.prefix_attention(q, kp, vp, ks, vs, lens(s_len), tau)
+        att.lard_attn_device_status()
+        au.check(got, au.prefix(q, kp, vp, ks, vs, s_len, tau))
+
+
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_prefix_padding_may_hold_anything(att, dtype):
     q, kp, vp, ks, vs, tau = prefix_inputs(3, 4, 2, 2, 150, 100, 128, dtype, seed=3)
