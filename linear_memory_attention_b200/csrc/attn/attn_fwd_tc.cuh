@@ -470,6 +470,8 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             w1 = ptx::ex2(m1 - base);
             l_all = l * w0 + stats[256 * (1 - i) + 128 + row] * w1;
         }
+        // With no key nothing has waited for the stream's Q, whose place the rows below take.
+        if (!kByKeys && mine == 0) ptx::named_bar_sync(1 + i, 128);
         if (ok && !*abort_flag) {
             const float inv = l_all == 0.f ? 0.f : 1.f / l_all;
             w0 *= inv;

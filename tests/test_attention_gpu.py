@@ -140,6 +140,20 @@ def test_offsets_past_32_bits(att, n, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("n", [3, 60, 460])
+def test_many_rows_that_see_no_key(att, n, d, dtype):
+    """Every row of every head of an empty sequence: zeros and -infinity, beside ones that see some keys."""
+    q, k, v, do, tau = cross_inputs(6, 32, 2, n, 16, d, dtype, "bnhd", seed=17)
+    k_len = [14, -1, 0, 15, 0, 0]
+    got = att.cross_attention(q, k, v, tau, lens(k_len), dout=do)
+    for b in (1, 2, 4, 5):
+        assert not got["out"][b].any() and (got["lse"][b] == -math.inf).all()
+        assert not got["dq"][b].any() and not got["dk"][b].any() and not got["dv"][b].any()
+    assert got["out"][0].any() and got["dq"][3].any()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_shared_keys(att, dtype):
     """One key block for all sequences (batch stride 0) and for all heads (head stride 0)."""
     q, k, v, _, tau = cross_inputs(3, 4, 2, 33, 90, 64, dtype, seed=21)
