@@ -140,6 +140,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dq_tc_kernel(const __gr
         ptx::tmem_alloc(&ctrl->tmem_base, 512);
         ptx::tmem_relinquish();
     }
+    __syncwarp();  // one thread of some warps has been elsewhere; setmaxnreg wants whole warps
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -484,6 +485,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         ptx::tmem_alloc(&ctrl->tmem_base, 512);
         ptx::tmem_relinquish();
     }
+    __syncwarp();  // one thread of some warps has been elsewhere; setmaxnreg wants whole warps
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();

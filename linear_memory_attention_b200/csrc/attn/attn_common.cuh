@@ -151,6 +151,16 @@ __device__ __forceinline__ void stage_bf16(uint32_t area, int lane, int first, c
 // What rounding to bf16 leaves of x.
 __device__ __forceinline__ float rounding_rest(float x) { return x - __bfloat162float(__float2bfloat16_rn(x)); }
 
+// The same of 32 values, in pairs (a conversion of two costs what one of one does).
+__device__ __forceinline__ void leave_rest(float (&o)[32]) {
+#pragma unroll
+    for (int k = 0; k < 32; k += 2) {
+        const uint32_t w = ptx::pack_bf16x2(o[k], o[k + 1]);
+        o[k] -= __uint_as_float(w << 16);
+        o[k + 1] -= __uint_as_float(w & 0xffff0000u);
+    }
+}
+
 // Writes 32 fp32 columns of a warp's 32 rows, COLS at a time through the area.
 template <int COLS>
 __device__ __forceinline__ void fp32_rows_out(uint32_t area, int lane, const float (&o)[32], float* mine) {

@@ -151,7 +151,41 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
     auto key_of = [&](int tile) { return (tile < tiles0 ? tile : tile - tiles0) * KT; };
     auto is_tail = [&](int tile) { return (tile < tiles0 ? len0 : len1) - key_of(tile) < KT; };
     constexpr int kTiles = kByKeys ? 2 : 1;  // K (and V) tiles of a step
+    // The row of a softmax thread: stream i, row `row` of its tile.
+    struct Row {
+        bool in;
+        int b, head, pos, rem;
+    };
+    auto row_of = [&](int i, int row) {
+        const int Gn = g.G * g.n, r = r0 + (kByKeys ? 0 : i * 128) + row;
+        Row x;
+        x.in = r < g.R;
+        x.b = pb + (x.in ? r / Gn : 0);
+        x.rem = x.in ? r % Gn : 0;
+        x.head = hk * g.G + x.rem / g.n;
+        x.pos = x.rem % g.n;
+        return x;
+    };
+    auto load_tile = [&](int slot, int tile, bool is_v) {  // one thread
+        const TcSeg& seg = g.seg[seg_of(tile)];
+        uint8_t* dst = smem + L::OFF_KV + slot * L::KV_TILE;
+        ptx::mbar_arrive_expect_tx(&ctrl->kv_full[slot], L::KV_TILE);
+        for (int c = 0; c < L::KC; ++c)
+            tma_load_4d(dst + c * KT * 128, is_v ? &seg.v : &seg.k, &ctrl->kv_full[slot], c * 64, key_of(tile),
+                        (is_v ? seg.vhead : seg.khead) ? hk : 0, (is_v ? seg.vbatch : seg.kbatch) ? pb : 0);
+    };
 
+    // What the first products read is requested before all else (it takes as long as the
+    // rest of the set-up): Q, rows past the end as zeros (by keys the two streams share
+    // one tile and the work), and the first step's K.
+    const int primed = S == 0 ? 0 : (kByKeys && steps(1) > 0 ? 2 : 1);
+    if (warp >= 4) {
+        const int q4 = warp & 3, i = (warp - 4) >> 2;
+        const Row x = row_of(i, q4 * 32 + lane);
+        rows_to_operand<D>(ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE), q4 * 32,
+                           x.in ? g.q.row(x.b, x.head, x.pos) : nullptr, lane, kByKeys ? 16 * i : 0, kByKeys ? 16 * i + 16 : 32);
+        copy_commit();
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < L::NS; ++s) {
             ptx::mbar_init(&ctrl->kv_full[s], 1);
@@ -167,8 +201,10 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
         }
         ctrl->abort_flag = 0;
         ptx::fence_mbar_init();
+        ptx::fence_proxy_async_smem();
+        for (int i = 0; i < primed; ++i) load_tile(i, tile_of(0, i), false);
     }
-    if (warp == 0 && lane == 0)
+    if (warp == 3 && lane == 0)
         for (int s = 0; s < g.nseg; ++s) {
             ptx::prefetch_tensormap(&g.seg[s].k);
             ptx::prefetch_tensormap(&g.seg[s].v);
@@ -177,6 +213,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
         ptx::tmem_alloc(&ctrl->tmem_base, L::TMEM_COLS);
         ptx::tmem_relinquish();
     }
+    __syncwarp();  // one thread of some warps has been elsewhere; setmaxnreg wants whole warps
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
@@ -188,28 +225,21 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
       if (warp == 0) {
         // ------------------------------------------------------------ producer
         // Ring order: the K tiles of step 0, its V tiles, the K tiles of step 1, ...
-        int slot = 0, round = 0, issued = 0;
+        int slot = 0, round = 0, issued = 0;  // units of the ring, the primed ones among them
         bool ok = true;
         for (int t = 0; ok && t < S; ++t) {
             for (int u = 0; ok && u < 2 * kTiles; ++u) {
                 const int i = u % kTiles;
                 const bool is_v = u >= kTiles;
                 if (kByKeys && t >= steps(i)) continue;
-                ok = mbar_wait(&ctrl->kv_empty[slot], (round & 1) ^ 1, abort_flag, lim, &g_lard_fault,
-                                    kFaultFwdProducer);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                if (lane == 0) {
-                    const int tile = tile_of(t, i);
-                    const TcSeg& seg = g.seg[seg_of(tile)];
-                    uint8_t* dst = smem + L::OFF_KV + slot * L::KV_TILE;
-                    ptx::mbar_arrive_expect_tx(&ctrl->kv_full[slot], L::KV_TILE);
-                    for (int c = 0; c < L::KC; ++c)
-                        tma_load_4d(dst + c * KT * 128, is_v ? &seg.v : &seg.k, &ctrl->kv_full[slot], c * 64,
-                                    key_of(tile), (is_v ? seg.vhead : seg.khead) ? hk : 0,
-                                    (is_v ? seg.vbatch : seg.kbatch) ? pb : 0);
+                if (issued >= primed) {  // else requested already, and by now perhaps even released again
+                    ok = mbar_wait(&ctrl->kv_empty[slot], (round & 1) ^ 1, abort_flag, lim, &g_lard_fault,
+                                   kFaultFwdProducer);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    if (lane == 0) load_tile(slot, tile_of(t, i), is_v);
+                    __syncwarp();
                 }
-                __syncwarp();
                 ++issued;
                 if (is_v && is_tail(tile_of(t, i))) {  // values past the sequence's end: zeros
                     const int tile = tile_of(t, i);
@@ -339,20 +369,13 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
         const int q4 = warp & 3;
         const int i = (warp - 4) >> 2;  // stream
         const int row = q4 * 32 + lane;
-        const int r = r0 + (kByKeys ? 0 : i * 128) + row;
-        const bool row_ok = r < g.R;
-        const int Gn = g.G * g.n;
-        const int b = pb + (row_ok ? r / Gn : 0), rem = row_ok ? r % Gn : 0;
-        const int head = hk * g.G + rem / g.n, pos = rem % g.n;
-        // Q into shared memory, rows past the end as zeros; by keys the two streams
-        // share one tile and the work.
-        rows_to_operand<D>(ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? 0 : i * L::TILE), q4 * 32,
-                           row_ok ? g.q.row(b, head, pos) : nullptr, lane, kByKeys ? 16 * i : 0, kByKeys ? 16 * i + 16 : 32);
-        copy_commit();
         copy_wait<0>();
         ptx::fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) ptx::mbar_arrive(&ctrl->q_ready);
+        const Row x = row_of(i, row);
+        const bool row_ok = x.in;
+        const int b = x.b, head = x.head, pos = x.pos;
         const uint32_t lane_base = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         const uint32_t ts = lane_base + i * KT, to = lane_base + L::TMEM_O + i * L::TMEM_O_STEP;
         const float cf = g.cfac;
@@ -477,7 +500,7 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             w0 *= inv;
             w1 *= inv;
             const float lse = l_all == 0.f ? -INFINITY : (m_all + log2f(l_all)) * kLn2;
-            const long long grow = (static_cast<long long>(b) * g.Hkv + hk) * Gn + rem;
+            const long long grow = (static_cast<long long>(b) * g.Hkv + hk) * g.G * g.n + x.rem;
             const long long prow = (g.split0 + split) * g.rows + grow;
             const bool other = kByKeys && steps(1 - i) > 0;
             // This thread's columns [col0, col0 + kCols), through the warp's share of Q's
@@ -485,37 +508,37 @@ __global__ void __launch_bounds__(kFwdTcThreads, (FwdTcLayout<D, kByKeys>::BLOCK
             constexpr int kCols = kByKeys ? D / 2 : D, kPart = kByKeys ? D / 4 : 32;
             const int col0 = kByKeys ? i * (D / 2) : 0;
             const uint32_t area = ptx::smem_u32(smem + L::OFF_Q) + (kByKeys ? (4 * i + q4) * (L::TILE / 8) : i * L::TILE + q4 * (L::TILE / 4));
-            // Loops that are not unrolled: short calls wait for instructions here.
+            __nv_bfloat16* out = row_ok && !g.join ? g.out.row(b, head, pos) : nullptr;
+            __nv_bfloat16* rest = row_ok && !g.join && g.rest.p ? g.rest.row(b, head, pos) : nullptr;
+            // A loop that is not unrolled: short calls wait for instructions here.
 #pragma unroll 1
-            for (int pass = 0; pass < (g.rest.p && !g.join ? 2 : 1); ++pass) {
-                const bool rest = pass == 1;
-#pragma unroll 1
-                for (int c = 0; c < kCols; c += 32) {
-                    float o[32];
-                    __syncwarp();
-                    if (mine > 0) {
-                        ptx::tmem_ld32(to + col0 + c, o);
-                        ptx::tmem_ld_wait(o);
+            for (int c = col0; c < col0 + kCols; c += 32) {
+                float o[32];
+                __syncwarp();
+                if (mine > 0) {
+                    ptx::tmem_ld32(to + c, o);
+                    ptx::tmem_ld_wait(o);
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] *= w0;
-                    } else {
+                    for (int k = 0; k < 32; ++k) o[k] *= w0;
+                } else {
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = 0.f;
-                    }
-                    if (other) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(col0 + c + k) * 128 + row], w1, o[k]);
-                    }
-                    if (rest) {
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = rounding_rest(o[k]);
-                    }
-                    if (g.join)
-                        fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + col0 + c : nullptr);
-                    else
-                        stage_bf16<kCols * 2>(area, lane, c / 8, o, 1.f);
+                    for (int k = 0; k < 32; ++k) o[k] = 0.f;
                 }
-                if (!g.join) staged_rows_out<kCols * 2>(area, row_ok ? (rest ? g.rest : g.out).row(b, head, pos) + col0 : nullptr, lane);
+                if (other) {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = fmaf(stage[(c + k) * 128 + row], w1, o[k]);
+                }
+                if (g.join) {
+                    fp32_rows_out<kPart>(area, lane, o, row_ok ? g.part_o + prow * D + c : nullptr);
+                    continue;
+                }
+                stage_bf16<64>(area, lane, 0, o, 1.f);
+                staged_rows_out<64>(area, row_ok ? out + c : nullptr, lane);
+                if (g.rest.p) {
+                    leave_rest(o);
+                    stage_bf16<64>(area, lane, 0, o, 1.f);
+                    staged_rows_out<64>(area, row_ok ? rest + c : nullptr, lane);
+                }
             }
             if (row_ok && (!kByKeys || i == 0)) {
                 if (g.join) g.part_lse[prow] = lse;
