@@ -23,6 +23,10 @@
 // 1000 W cap 1.02 ms); 4 x 4096 x 4096, d = 64: 765 us, 718 TFLOP/s, where the
 // exponential unit is the nearer bound (tiles of 64 keys and two blocks an SM: 20 %
 // over tiles of 128 and one).
+// A block's beginning and end take some 16000 cycles beside its steps: 2000 to set up (Q
+// and the first K come meanwhile), 1500 to the first S, a first softmax 3000 longer than
+// the others (instructions not cached yet), 900 for the last P V, 4000 to 5000 to write its rows, 1600
+// between two blocks of an SM.
 // Tried and slower at d = 128: four softmax warpgroups; part of the exponentials on
 // the FMA pipe; units of 64 keys with two S a stream (1.25 ms); one stream a block
 // and two blocks an SM (10 %).
