@@ -15,6 +15,7 @@ built.  Functions with the C names take the caller's buffers:
 and two that allocate what they return (and the workspace):
     cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None)
     prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream=None)
+stream is a torch stream or a raw handle of the inputs' GPU; None: its current one.
 Tensors are torch tensors on one GPU, bf16 or fp32, [B, H, rows, d] by shape; in memory
 any batch, head and row strides that are multiples of 16 bytes, the last dimension
 contiguous (so x.transpose(1, 2) of a [B, rows, H, d] tensor is taken as it is).
@@ -245,10 +246,11 @@ def lard_prefix_attn(q, kp, vp, ks, vs, s_len, tau, out, lse, workspace=None, st
     _call(_lib.lard_prefix_attn, "lard_prefix_attn", args, workspace, need, q, stream)
 
 
-def _on(stream):
-    """A context in which what is allocated belongs to the stream of the call."""
+def _on(stream, q):
+    """A context in which what is allocated on q's GPU belongs to the given stream.  A raw handle
+    is one of q's GPU, which need not be the current one."""
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream))
+        stream = torch.cuda.ExternalStream(int(stream), device=q.device)
     return torch.cuda.stream(stream)
 
 
@@ -268,8 +270,12 @@ def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
     Returns a dict with out (q's dtype and layout), lse [B, Hq, n] and, with dout, dq, dk, dv.
     """
     if stream is not None:
-        with _on(stream):
-            return cross_attention(q, k, v, tau, k_len, dout)
+        with _on(stream, q):
+            return _cross_attention(q, k, v, tau, k_len, dout, stream)
+    return _cross_attention(q, k, v, tau, k_len, dout, None)
+
+
+def _cross_attention(q, k, v, tau, k_len, dout, stream):
     if q.dim() != 4:
         raise ValueError("q must be [B, H, rows, d]")
     out, lse = _outputs(q)
@@ -277,11 +283,11 @@ def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
     rest = torch.empty_like(q) if grads is not None and q.dtype is torch.bfloat16 else None
     args = _cross_args(q, k, v, tau, k_len, out, lse, grads, rest)
     need = _lib.lard_cross_attn_fwd_workspace_bytes(args)
-    _call(_lib.lard_cross_attn_fwd, "lard_cross_attn_fwd", args, _bytes(need, q), need, q, None)
+    _call(_lib.lard_cross_attn_fwd, "lard_cross_attn_fwd", args, _bytes(need, q), need, q, stream)
     got = {"out": out, "lse": lse}
     if grads is not None:
         need = _lib.lard_cross_attn_bwd_workspace_bytes(args)
-        _call(_lib.lard_cross_attn_bwd, "lard_cross_attn_bwd", args, _bytes(need, q), need, q, None)
+        _call(_lib.lard_cross_attn_bwd, "lard_cross_attn_bwd", args, _bytes(need, q), need, q, stream)
         got["dq"], got["dk"], got["dv"] = grads[1:]
     return got
 
@@ -289,14 +295,18 @@ def cross_attention(q, k, v, tau, k_len=None, dout=None, stream=None):
 def prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream=None):
     """Allocate the outputs and run lard_prefix_attn: returns a dict with out and lse."""
     if stream is not None:
-        with _on(stream):
-            return prefix_attention(q, kp, vp, ks, vs, s_len, tau)
+        with _on(stream, q):
+            return _prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream)
+    return _prefix_attention(q, kp, vp, ks, vs, s_len, tau, None)
+
+
+def _prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream):
     if q.dim() != 4:
         raise ValueError("q must be [B, H, rows, d]")
     out, lse = _outputs(q)
     args = _prefix_args(q, kp, vp, ks, vs, s_len, tau, out, lse)
     need = _lib.lard_prefix_attn_workspace_bytes(args)
-    _call(_lib.lard_prefix_attn, "lard_prefix_attn", args, _bytes(need, q), need, q, None)
+    _call(_lib.lard_prefix_attn, "lard_prefix_attn", args, _bytes(need, q), need, q, stream)
     return {"out": out, "lse": lse}
 
 

@@ -1,10 +1,12 @@
 """CPU checks of the attention library's C ABI: it exports what include/lard_attn.h declares
 and refuses bad arguments before any CUDA call (the addresses below are made up)."""
+import contextlib
 import ctypes
 import os
 import re
 import subprocess
 import sys
+import types
 
 import pytest
 import torch
@@ -187,6 +189,60 @@ def test_binding_refuses(att):
         att.lard_prefix_attn(q, z(3, 9, 64), z(3, 9, 64), k, k, None, 0.1, out, lse)
     with pytest.raises(ValueError):
         att.lard_prefix_attn(q, k, k, k, k, None, 0.1, out, lse)
+
+
+class _OnGpu1(torch.Tensor):
+    """A host tensor that says it is on GPU 1."""
+
+    def get_device(self):
+        return 1
+
+    @property
+    def device(self):
+        return torch.device("cuda", 1)
+
+
+class _Streams:
+    """Stands in for torch's streams, with GPU 0 current: which stream is current on each GPU."""
+
+    def __init__(self):
+        self.gpu, self.at = 0, {0: 0xA0, 1: 0xA1}
+
+    def external(self, handle, device=None):
+        gpu = self.gpu if device is None else torch.device(device).index
+        return types.SimpleNamespace(cuda_stream=handle, device=torch.device("cuda", gpu))
+
+    @contextlib.contextmanager
+    def use(self, stream):
+        before = self.gpu, dict(self.at)
+        self.gpu, self.at[stream.device.index] = stream.device.index, stream.cuda_stream
+        yield
+        self.gpu, self.at = before
+
+
+@pytest.mark.parametrize("given", ["raw handle", "stream", "none"])
+@pytest.mark.parametrize("call", ["forward", "training step", "prefix"])
+def test_work_goes_to_the_given_stream(att, monkeypatch, call, given):
+    """The allocating calls enqueue on the stream that they are given, and allocate for it,
+    also where the inputs are on a GPU that is not the current one."""
+    streams, enqueued, allocated = _Streams(), [], []
+    for name in ("lard_cross_attn_fwd", "lard_cross_attn_bwd", "lard_prefix_attn"):
+        monkeypatch.setattr(att._lib, name, lambda args, ws, size, stream: enqueued.append(stream) or 0)
+    monkeypatch.setattr(att, "_raw_stream", lambda gpu: streams.at[gpu])
+    monkeypatch.setattr(torch.cuda, "ExternalStream", streams.external)
+    monkeypatch.setattr(torch.cuda, "stream", streams.use)
+    monkeypatch.setattr(torch, "empty_strided", lambda size, stride, device, dtype: allocated.append(
+        streams.at[device.index]) or torch.zeros(size, dtype=dtype).as_subclass(_OnGpu1))
+    z = lambda *s: torch.zeros(s, dtype=torch.bfloat16).as_subclass(_OnGpu1)  # noqa: E731
+    q, k = z(2, 4, 5, 64), z(2, 2, 7, 64)
+    stream = {"raw handle": 0xC0DE, "stream": streams.external(0xC0DE, "cuda:1"), "none": None}[given]
+    if call == "prefix":
+        att.prefix_attention(q, k[0], k[0], k, k, None, 0.1, stream=stream)
+    else:
+        att.cross_attention(q, k, k, 0.1, dout=q if call == "training step" else None, stream=stream)
+    assert enqueued == [0xA1 if stream is None else 0xC0DE] * (2 if call == "training step" else 1)
+    assert allocated and set(allocated) == set(enqueued)
+    assert (streams.gpu, streams.at) == (0, {0: 0xA0, 1: 0xA1})
 
 
 def test_workspace_grows_with_what_is_split(att):

@@ -383,6 +383,27 @@ def test_two_streams_at_once(att):
         att.lard_attn_device_status(s)
 
 
+@pytest.mark.parametrize("raw", [False, True], ids=["stream", "handle"])
+def test_calls_follow_the_given_stream(att, raw):
+    """Inputs that the given stream is still to write, behind some 50 ms of other work, while the
+    current stream is idle: the calls come after them."""
+    q, k, v, do, tau = cross_inputs(2, 4, 2, 33, 170, 64, BF16, seed=161)
+    late = [torch.zeros_like(x) for x in (q, k, v, do)]
+    side = torch.cuda.Stream()
+    given = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)
+        for x, y in zip(late, (q, k, v, do)):
+            x.copy_(y)
+    got = att.cross_attention(*late[:3], tau, dout=late[3], stream=given)
+    shared = att.prefix_attention(late[0], late[1][0], late[2][0], None, None, None, tau, stream=given)
+    assert torch.cuda.current_stream() != side
+    att.lard_attn_device_status(given)
+    au.check(got, au.cross(q, k, v, tau, None, do))
+    au.check(shared, au.cross(q, k[:1].expand(2, -1, -1, -1), v[:1].expand(2, -1, -1, -1), tau))
+
+
 def test_interleaved_outputs(att):
     """dK and dV as the two halves of one [B, m, 2, H, d] buffer, as a fused projection has it."""
     q, k, v, do, tau = cross_inputs(2, 4, 2, 20, 90, 64, BF16, seed=141)
