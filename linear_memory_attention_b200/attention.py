@@ -28,7 +28,7 @@ import struct
 
 import torch
 
-from .lard import LARD_DTYPE_BF16, LARD_DTYPE_FP32, LARD_OK, LardError
+from .lard import LARD_DTYPE_BF16, LARD_DTYPE_FP32, LARD_OK, LardError, _gpu_of
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "liblard_attn.so")
@@ -311,10 +311,12 @@ def _prefix_attention(q, kp, vp, ks, vs, s_len, tau, stream):
 
 
 def lard_attn_device_status(stream=None) -> int:
-    """Synchronise the stream and check the kernels' fault word; raises on a timed-out wait."""
+    """Synchronise the stream and check the kernels' fault word on its GPU; raises on a
+    timed-out wait."""
     bits = ctypes.c_uint(0)
-    handle = torch.cuda.current_stream().cuda_stream if stream is None else _handle(stream, None)
-    st = _lib.lard_attn_device_status(handle, ctypes.byref(bits))
+    with _gpu_of(stream):
+        handle = torch.cuda.current_stream().cuda_stream if stream is None else _handle(stream, None)
+        st = _lib.lard_attn_device_status(handle, ctypes.byref(bits))
     if st != LARD_OK:
         err = LardError(st, f"lard_attn_device_status (fault bits 0x{bits.value:x})")
         err.fault_bits = bits.value

@@ -24,6 +24,7 @@ the bf16 gradients of lard_kl_bwd_multi_bf16), contiguous, on the GPU that runs 
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 
@@ -388,10 +389,20 @@ def relations_kl(pairs, tau, causal=True, grad_scale=1.0, backward=True, fused_s
     return outs, loss
 
 
+def _gpu_of(stream):
+    """A context in which a torch stream's GPU is current: the default stream's handle is 0 on
+    every GPU, and 0 stands for the current GPU's."""
+    import torch
+    device = getattr(stream, "device", None)
+    return contextlib.nullcontext() if device is None else torch.cuda.device(device)
+
+
 def lard_device_status(stream=None) -> int:
-    """Synchronise the stream and check the kernels' fault word; raises on a timed-out wait."""
+    """Synchronise the stream and check the kernels' fault word on its GPU; raises on a
+    timed-out wait."""
     bits = ctypes.c_uint(0)
-    st = _lib.lard_device_status(_stream(stream), ctypes.byref(bits))
+    with _gpu_of(stream):
+        st = _lib.lard_device_status(_stream(stream), ctypes.byref(bits))
     if st != LARD_OK:
         err = LardError(st, f"lard_device_status (fault bits 0x{bits.value:x})")
         err.fault_bits = bits.value

@@ -245,6 +245,29 @@ def test_work_goes_to_the_given_stream(att, monkeypatch, call, given):
     assert (streams.gpu, streams.at) == (0, {0: 0xA0, 1: 0xA1})
 
 
+@pytest.mark.parametrize("binding", ["attention", "lard"])
+def test_status_is_read_on_the_streams_gpu(att, monkeypatch, binding):
+    """The default stream's handle is 0 on every GPU, and the library takes 0 for the current
+    GPU's: the binding makes the stream's GPU current."""
+    from linear_memory_attention_b200 import lard
+    module, name = (att, "lard_attn_device_status") if binding == "attention" else (lard, "lard_device_status")
+    gpu, seen = [0], []
+
+    @contextlib.contextmanager
+    def device(which):
+        before, gpu[0] = gpu[0], torch.device(which).index
+        yield
+        gpu[0] = before
+
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: stream(0xA0, gpu[0]))
+    monkeypatch.setattr(module._lib, name, lambda handle, bits: seen.append((getattr(handle, "value", handle) or 0, gpu[0])) or 0)
+    stream = lambda handle, at: types.SimpleNamespace(cuda_stream=handle, device=torch.device("cuda", at))  # noqa: E731
+    for given in (stream(0, 1), stream(0xC0DE, 1), stream(0, 0), None, 0xC0DE, 0):
+        getattr(module, name)(given)
+    assert seen == [(0, 1), (0xC0DE, 1), (0, 0), (0xA0, 0), (0xC0DE, 0), (0, 0)] and gpu == [0]
+
+
 def test_workspace_grows_with_what_is_split(att):
     """Few rows over many keys are split over blocks, whose partial rows need room; enough
     rows need none."""
