@@ -336,6 +336,131 @@ def test_forward_is_deterministic(att):
                 assert torch.equal(first["out"], again["out"]) and torch.equal(first["lse"], again["lse"])
 
 
+class Guarded:
+    """Buffers with guard bytes on either side of each."""
+
+    def __init__(self):
+        self.all = []
+
+    def empty(self, shape, dtype):
+        size = math.prod(shape) * dtype.itemsize
+        raw = torch.full((size + 512,), 0xA5, dtype=torch.uint8, device="cuda")
+        self.all.append((raw, size))
+        return raw[256:256 + size].view(dtype).view(shape)
+
+    def check(self):
+        for raw, size in self.all:
+            assert (raw[:256] == 0xA5).all() and (raw[256 + size:] == 0xA5).all()
+
+
+def parts(need, rows, d):
+    """Parts of each row that a forward call of this workspace joins."""
+    return need // (rows * (4 * d + 4))
+
+
+# From 8192 rows on a warp joins eight rows; neither count is a multiple of eight.
+# (B, Hq, Hkv, n, P, S): two parts a row; nine (five at d = 128 in bf16), which four lanes share.
+@pytest.mark.parametrize("case", [(3, 7, 7, 391, 70, 50), (51, 7, 1, 23, 3000, 30)], ids=["two parts", "many parts"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_join_of_many_rows(att, case, dtype, d):
+    B, Hq, Hkv, n, P, S = case
+    q, kp, vp, ks, vs, tau = prefix_inputs(B, Hq, Hkv, n, P, S, d, dtype, "bnhd", seed=d + P)
+    s_len = [(S + 7 * b) % (S + 1) for b in range(B)]
+    need = att.lard_prefix_attn_workspace_bytes(q, kp, ks)
+    assert B * Hq * n > 8192 and B * Hq * n % 8 and (parts(need, B * Hq * n, d) == 2) == (P == 70)
+    guard = Guarded()
+    got = {"out": guard.empty(q.shape, dtype), "lse": guard.empty((B, Hq, n), FP32)}
+    att.lard_prefix_attn(q, kp, vp, ks, vs, lens(s_len), tau, got["out"], got["lse"], guard.empty((need,), torch.uint8))
+    att.lard_attn_device_status()
+    au.check(got, au.prefix(q, kp, vp, ks, vs, s_len, tau))
+    guard.check()
+
+
+@pytest.mark.parametrize("dtype,m", [(BF16, 1000), (FP32, 3000)], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("size", [900, 30, 0])
+def test_join_of_many_rows_with_rest(att, dtype, m, d, size):
+    """The same join of one long sequence's rows, with what rounding leaves of them; of the shorter
+    lengths most parts, or all, have seen nothing."""
+    n = 8203
+    q, k, v, _, tau = cross_inputs(1, 1, 1, n, m, d, dtype, seed=181)
+    need = att.lard_cross_attn_fwd_workspace_bytes(q, k)
+    assert parts(need, n, d) >= 4
+    guard = Guarded()
+    got = {"out": guard.empty(q.shape, dtype), "lse": guard.empty((1, 1, n), FP32)}
+    if dtype is BF16:
+        got["rest"] = guard.empty(q.shape, dtype)
+    att.lard_cross_attn_fwd(q, k, v, tau, got["out"], got["lse"], lens([size]), guard.empty((need,), torch.uint8),
+                            rest=got.get("rest"))
+    att.lard_attn_device_status()
+    if dtype is BF16:
+        got["sum"] = got["out"].double() + got["rest"].double()
+    au.check(got, au.cross(q, k, v, tau, [size], rest=dtype is BF16))
+    guard.check()
+
+
+# Few problems of many keys: several clusters of blocks share a problem's keys in bf16.
+@pytest.mark.parametrize("case", [(2, 8, 2, 1, 17000, [17000, 40]), (1, 8, 1, 2, 40000, [39999]),
+                                  (1, 4, 1, 4, 40000, [21]), (4, 4, 1, 3, 20000, [20000, 0, 333, 9001])],
+                         ids=lambda c: "x".join(map(str, c[:5])))
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_few_rows_over_very_many_keys(att, case, dtype, d):
+    B, Hq, Hkv, n, m, k_len = case
+    q, k, v, _, tau = cross_inputs(B, Hq, Hkv, n, m, d, dtype, "bnhd", seed=191)
+    need = att.lard_cross_attn_fwd_workspace_bytes(q, k)
+    assert parts(need, B * Hq * n, d) >= 2
+    guard = Guarded()
+    got = {"out": guard.empty(q.shape, dtype), "lse": guard.empty((B, Hq, n), FP32)}
+    if dtype is BF16:
+        got["rest"] = guard.empty(q.shape, dtype)
+    att.lard_cross_attn_fwd(q, k, v, tau, got["out"], got["lse"], lens(k_len), guard.empty((need,), torch.uint8),
+                            rest=got.get("rest"))
+    att.lard_attn_device_status()
+    au.check(got, au.cross(q, k, v, tau, k_len))
+    guard.check()
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_one_token_behind_a_very_long_prefix(att, dtype):
+    """The clusters' runs of keys pass from the shared rows to the sequence's own."""
+    for P, S, s_len in ((20001, 77, [50]), (13, 20000, [19990])):
+        q, kp, vp, ks, vs, tau = prefix_inputs(1, 8, 2, 2, P, S, 128, dtype, seed=195)
+        assert parts(att.lard_prefix_attn_workspace_bytes(q, kp, ks), 16, 128) >= 2
+        got = att.prefix_attention(q, kp, vp, ks, vs, lens(s_len), tau)
+        att.lard_attn_device_status()
+        au.check(got, au.prefix(q, kp, vp, ks, vs, s_len, tau))
+
+
+# Both axes split, one of them, neither (bf16); each with an empty tail.
+@pytest.mark.parametrize("B,Hq,Hkv,n,m", [(1, 4, 2, 200, 900), (1, 4, 2, 5, 7000), (4, 10, 10, 500, 520)])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_gradients_repeat_bit_for_bit(att, B, Hq, Hkv, n, m, dtype):
+    q, k, v, do, tau = cross_inputs(B, Hq, Hkv, n, m, 128, dtype, "bnhd", seed=201)
+    k_len = lens([m - 30 * (b + 1) for b in range(B)])
+    first = att.cross_attention(q, k, v, tau, k_len, dout=do)
+    for _ in range(4):
+        again = att.cross_attention(q, k, v, tau, k_len, dout=do)
+        for name in first:
+            assert torch.equal(first[name], again[name]), name
+    assert first["dq"].any() and first["dk"].any() and first["dv"].any()
+
+
+@pytest.mark.parametrize("n", [6, 150])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_gradients_of_shared_inputs(att, n, dtype):
+    """Queries and upstream gradients shared by all heads, keys by all sequences, values by all
+    key heads (strides of 0): the gradients are those of every sequence and head."""
+    B, Hq, Hkv, m, d = 3, 4, 2, 140, 64
+    q, k, v, do, tau = cross_inputs(B, Hq, Hkv, n, m, d, dtype, seed=211)
+    q, do = q[:, :1].expand(B, Hq, n, d), do[:1, :1].expand(B, Hq, n, d)
+    k, v = k[:1].expand(B, Hkv, m, d), v[:, :1].expand(B, Hkv, m, d)
+    got = att.cross_attention(q, k, v, tau, lens([140, 0, 77]), dout=do)
+    att.lard_attn_device_status()
+    au.check(got, au.cross(q, k, v, tau, [140, 0, 77], do))
+
+
 def test_captured_calls_replay_with_other_lengths(att):
     """Forward, backward and prefix calls in one graph; replays follow the lengths and inputs
     in device memory.  An eager call in between uses memory of its own."""
