@@ -437,6 +437,10 @@ static_assert(sizeof(DkvCtrl) <= 4096, "control block too large");
 // Descriptor low-word step for K step kk of a 64-row, K-major unit (8 KB a 64-column chunk).
 __host__ __device__ constexpr uint32_t desc_step_k64(int kk) { return (kk >> 2) * (8192 >> 4) + (kk & 3) * (32 >> 4); }
 
+// It starts beside dQ's last blocks and needs their delta.  How long those take is not this
+// kernel's affair, so every role waits for that kernel's end before its first bounded wait
+// that something formed from delta has to end; K, V, the first units and the first
+// two S^T and dP^T come before that.
 // Grid: key tiles of m (fastest), splits of the rows, B * Hkv.
 template <int D>
 __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __grid_constant__ TcBwdArgs g) {
@@ -507,6 +511,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         int issued = 0;
         for (int u = 0; u < U; ++u) {
             const int s = u % L::NS;
+            if (u == L::NS) wait_for_kernel_before();  // no stage is free again before delta is there
             const bool ok = mbar_wait(&ctrl->u_empty[s], ((u / L::NS) & 1) ^ 1, abort_flag, lim, &g_lard_fault,
                                            kFaultBwdProducer);
             if (!__all_sync(0xffffffffu, ok)) break;
@@ -579,6 +584,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
             };
             bool ok = U > 0 && wait(&ctrl->kv_full, 0);
             for (int u = 0; ok && u < 2 && u < U; ++u) ok = issue_s(u);
+            wait_for_kernel_before();  // P^T and dZ^T come after delta
             int s = 0;
             for (int u = 0; ok && u < U; ++u) {
                 const int stream = u & 1;
@@ -613,6 +619,7 @@ __global__ void __launch_bounds__(kBwdTcThreads, 1) attn_dkdv_tc_kernel(const __
         const uint32_t ts = lane_base + 256 + i * 64, tp = ts + 128;
         const float2 cf2 = splat2(g.cfac);
         bool ok = true;
+        wait_for_kernel_before();  // each unit's statistics come after delta
         for (int u = i; u < U; u += 2) {
             const int s = u % L::NS;
             ok = mbar_wait(&ctrl->st_full[s], (u / L::NS) & 1, abort_flag, lim, &g_lard_fault, kFaultBwdSoftmax) &&
