@@ -35,6 +35,17 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&x)[E
     else *reinterpret_cast<uint32_t*>(p) = ptx::pack_bf16x2(x[0], x[1]);
 }
 
+// First row of a warp of a join: 256 threads a block, rpw rows a warp.  The number of a thread in
+// the grid would pass 32 bits from 2^30 rows on.
+constexpr int kJoinThreads = 256;
+__host__ __device__ constexpr unsigned join_row(unsigned block, unsigned thread, unsigned rpw) {
+    return (block * (kJoinThreads / 32) + thread / 32) * rpw;
+}
+static_assert(join_row(0, 95, 8) == 16 && join_row(2, 32, 1) == 17, "rows of the first warps");
+static_assert(join_row((1u << 24) - 1, 255, 8) == (1u << 30) - 8 && join_row(1u << 24, 0, 8) == 1u << 30 &&
+                  join_row((0x7fffffffu - 1) / 64, 255, 8) == 0x7ffffff8u,
+              "rows of the last warps");
+
 // Joins the splits of a row: LSE = log sum_s exp LSE_s, O = sum_s exp(LSE_s - LSE) O_s.
 // A warp has RPW rows (1 or 8): its lanes share the rows' weights, LPR lanes a row, then
 // row by row the head dimension, with the parts of four splits requested at a time.
@@ -43,12 +54,12 @@ __device__ __forceinline__ void store_piece(__nv_bfloat16* p, const float (&x)[E
 // with eight.  Few rows are left to a warp each, and the first parts are requested
 // before the weights are known.
 template <typename T, int D, int RPW>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ FwdArgs<T> g) {
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(const __grid_constant__ FwdArgs<T> g) {
     wait_for_kernel_before();
     constexpr int E = D / 32, LPR = 32 / RPW, kBatch = 4;
     const int lane = threadIdx.x & 31, sub = lane % LPR;
     const unsigned rows = static_cast<unsigned>(g.rows);  // below 2^31 where there is a join
-    const unsigned row0 = (blockIdx.x * blockDim.x + threadIdx.x) / 32 * RPW, row = row0 + lane / LPR;
+    const unsigned row0 = join_row(blockIdx.x, threadIdx.x, RPW), row = row0 + lane / LPR;
     if (row0 >= rows) return;
     const bool in = row < rows;
     const float* part = g.part_o + static_cast<size_t>(row0) * D + lane * E;

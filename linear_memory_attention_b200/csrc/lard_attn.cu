@@ -581,8 +581,8 @@ lard_status run_fwd(const Fwd& f, const FwdPlan& p, void* ws, cudaStream_t strea
         split0 += x.splits;
     }
     if (!p.join()) return LARD_OK;
-    return p.rows >= kManyRows ? launch(attn_join_kernel<T, D, 8>, tiles_of(p.rows, 64), 256, 0, stream, true, 0, g)
-                               : launch(attn_join_kernel<T, D, 1>, tiles_of(p.rows, 8), 256, 0, stream, true, 0, g);
+    return p.rows >= kManyRows ? launch(attn_join_kernel<T, D, 8>, tiles_of(p.rows, 64), kJoinThreads, 0, stream, true, 0, g)
+                               : launch(attn_join_kernel<T, D, 1>, tiles_of(p.rows, 8), kJoinThreads, 0, stream, true, 0, g);
 }
 
 Fwd cross_work(const lard_cross_attn& a, const lard_attn_view* v = nullptr) {
