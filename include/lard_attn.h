@@ -47,7 +47,13 @@
  *   - Errors, streams, devices and bounded waits are as in lard.h; the fault word
  *     of these kernels is read with lard_attn_device_status.
  *   - 1 <= n, m, P, S <= 2^31 - 256 (P or S may be 0 for prefix attention, not
- *     both), Hq / Hkv * n < 2^31, B * Hq < 2^30.
+ *     both), Hq / Hkv * n <= 2^31 - 256, B * Hq < 2^30.  Prefix attention takes the
+ *     queries of all sequences together: B * Hq / Hkv * n <= 2^31 - 256.
+ *   - A launch has at most 2^31 - 1 blocks (a block has the rows, or keys, of one key head
+ *     of one sequence: in bf16 256 rows in the forward pass, 128 rows or keys in the
+ *     backward pass, in fp32 64; fewer where there are no more), and a forward call
+ *     that splits its keys, or has both shared and own keys, joins at most 2^31 - 1
+ *     rows (B * Hq * n).  A call that would need more is refused with LARD_ERR_INVALID_ARG.
  */
 #ifndef LARD_ATTN_H
 #define LARD_ATTN_H

@@ -156,6 +156,57 @@ def test_prefix_refuses(att, kw):
     assert prefix_call(att, **kw) == 1
 
 
+FAR = 1 << 46  # more than any tensor of the largest sizes
+
+
+def far(call):
+    """Addresses of a call so far apart that tensors of any size are disjoint."""
+    names = "q k v out dout dq dk dv" if call is cross_call else "q kp vp ks vs out"
+    return {f"{x}_ptr": (i + 1) * FAR for i, x in enumerate(names.split())} | dict(
+        lse=20 * FAR, ws=30 * FAR, **({"k_len": 22 * FAR} if call is cross_call else {"s_len": 22 * FAR}))
+
+
+END = 1 << 31
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kw,over", [
+    (dict(B=1, Hq=1, Hkv=1, n=END - 256), dict(n=END - 255)),
+    (dict(B=1, Hq=1, Hkv=1, n=1, m=END - 256), dict(m=END - 255)),
+    (dict(B=1, Hq=2, Hkv=1, n=END // 2 - 128), dict(n=END // 2 - 127)),
+    (dict(B=1 << 20, Hq=1023, Hkv=1023, n=1, m=1), dict(Hq=1024, Hkv=1024)),
+])
+def test_size_limits_of_cross_attention(att, dtype, kw, over):
+    """The header's limits are those of the checks, in both passes."""
+    end = 1 if torch.cuda.is_available() else 3
+    for fn in ("fwd", "bwd"):
+        assert cross_call(att, fn, **far(cross_call), **dict(kw, dtype=dtype)) == end
+        assert cross_call(att, fn, **far(cross_call), **dict(kw, dtype=dtype, **over)) == 1
+
+
+@pytest.mark.parametrize("fn,dtype,rows", [("fwd", 0, 256), ("bwd", 0, 128), ("fwd", 1, 64), ("bwd", 1, 64)])
+def test_limit_of_a_launchs_blocks(att, fn, dtype, rows):
+    end = 1 if torch.cuda.is_available() else 3
+    size = dict(Hq=1, Hkv=1, n=END - 256, dtype=dtype)  # (END - 256) / rows blocks a sequence
+    assert cross_call(att, fn, **far(cross_call), B=rows, **size) == end
+    assert cross_call(att, fn, **far(cross_call), B=rows + 1, **size) == 1
+
+
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("kw,over", [
+    (dict(B=1, Hq=1, Hkv=1, n=END - 256, S=0), dict(n=END - 255)),
+    (dict(B=1, Hq=1, Hkv=1, n=1, S=1, P=END - 256), dict(P=END - 255)),
+    (dict(B=1, Hq=1, Hkv=1, n=1, P=0, S=END - 256), dict(S=END - 255)),
+    (dict(B=2, Hq=2, Hkv=1, n=END // 4 - 64, S=0), dict(n=END // 4 - 63)),          # queries of a key head
+    (dict(B=1 << 20, Hq=1023, Hkv=1023, n=1, S=0), dict(Hq=1024, Hkv=1024)),
+    (dict(B=2, Hq=16, Hkv=16, n=END // 32 - 8), dict(n=END // 32)),                  # rows to join
+])
+def test_size_limits_of_prefix_attention(att, dtype, kw, over):
+    end = 1 if torch.cuda.is_available() else 3
+    assert prefix_call(att, **far(prefix_call), **dict(kw, dtype=dtype)) == end
+    assert prefix_call(att, **far(prefix_call), **dict(kw, dtype=dtype, **over)) == 1
+
+
 def test_null_arguments(att):
     assert att._lib.lard_cross_attn_fwd(None, None, 0, None) == 1
     assert att._lib.lard_cross_attn_bwd(None, None, 0, None) == 1
