@@ -33,7 +33,7 @@
 // Key tiles past a sequence's length are never visited.  Values of rows past
 // it inside the last tile are zeroed in shared memory before the product (0
 // times what is there could be NaN); their logits are replaced by -infinity.
-// TMEM: S of stream i at 128 i, O behind the streams' S.
+// TMEM: S of stream i at KT i, O in the upper half.
 // Roles:
 //   warp 0       TMA producer of the K / V ring
 //   warp 1       TMEM owner, MMA issuer

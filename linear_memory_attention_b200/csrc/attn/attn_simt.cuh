@@ -141,7 +141,7 @@ __device__ __forceinline__ void simt_accumulate(const float* W, const float* M, 
 
 __device__ __forceinline__ float4 scaled(float2 a, float2 b, float s) { return make_float4(a.x * s, a.y * s, b.x * s, b.y * s); }
 
-// Grid: row tiles of 8 RT rows (fastest), then splits, then problems.
+// Grid: row tiles of 16 RT rows (fastest), then splits, then problems.
 template <int D, int RT>
 __global__ void __launch_bounds__(kSimtThreads) attn_fwd_simt_kernel(const __grid_constant__ FwdArgs<float> g) {
     using L = SimtLayout<D>;
