@@ -1,4 +1,5 @@
-// dK and dV of the bf16 backward pass behind a slow kernel: launched by test_attention_waits.py.
+// Bounded waits of the attention kernels, launched by test_attention_waits.py.
+// dK and dV of the bf16 backward pass behind a slow kernel:
 // The library launches attn_dkdv_tc_kernel beside the last blocks of the kernel that forms
 // delta; here that one is replaced by a kernel that lets its successor start at once, takes
 // as long as it is told and only then writes delta.
@@ -76,4 +77,37 @@ extern "C" __attribute__((visibility("default"))) int dkdv_behind(int d, void* q
     auto f = [](void* p) { return static_cast<float*>(p); };
     return (d == 64 ? run<64> : run<128>)(h(q), h(k), h(v), h(dout), h(dk), h(dv), f(lse), f(from), f(delta), Hq, Hkv, n, m,
                                           tau, before_us, wait_us);
+}
+
+// What bounded waits do: got[0..3] = whether the wait returned true, microseconds that it took,
+// twice (an mbarrier that nothing arrives at; the same when the block has given up);
+// got[4] = an mbarrier whose phase is complete.  Then the exit wait runs out.
+__global__ void waits_run_out(unsigned long long ns, unsigned int* got) {
+    __shared__ uint64_t bar[2];
+    __shared__ int abort_flag;
+    if (threadIdx.x != 0) return;
+    abort_flag = 0;
+    lard::ptx::mbar_init(&bar[0], 1);
+    lard::ptx::mbar_init(&bar[1], 1);
+    lard::ptx::fence_mbar_init();
+    lard::ptx::mbar_arrive(&bar[1]);
+    for (int k = 0; k < 2; ++k) {
+        const uint64_t t0 = lard::ptx::globaltimer_ns();
+        got[2 * k] = mbar_wait(&bar[0], 0, &abort_flag, k ? 1000 * ns : ns, &lard::g_lard_fault, lard::kFaultBwdMma);
+        got[2 * k + 1] = static_cast<unsigned int>((lard::ptx::globaltimer_ns() - t0) / 1000);
+    }
+    got[4] = mbar_wait(&bar[1], 0, &abort_flag, ns, &lard::g_lard_fault, lard::kFaultBwdProducer);
+    lard::drain(&bar[0], 0, ns);
+}
+
+// Returns the fault bits, which it clears, or a negative number if a call failed.
+extern "C" __attribute__((visibility("default"))) int run_out(unsigned limit_us, unsigned int* got) {
+    waits_run_out<<<1, 32>>>(1000ull * limit_us, got);
+    if (cudaDeviceSynchronize() != cudaSuccess) return -1;
+    unsigned int fault = 0;
+    const unsigned int zero = 0;
+    if (cudaMemcpyFromSymbol(&fault, lard::g_lard_fault, sizeof(fault)) != cudaSuccess ||
+        cudaMemcpyToSymbol(lard::g_lard_fault, &zero, sizeof(zero)) != cudaSuccess)
+        return -2;
+    return static_cast<int>(fault);
 }
