@@ -281,6 +281,11 @@ struct FwdPlan {
 
 // How many blocks share a long axis of `steps` tiles when there are `blocks`
 // without: as many as fill the GPU once, where one set would leave it partly idle.
+// Measured, gradients at d = 128 (dQ blocks x dK, dV blocks; us): 64 x 64 (2 heads, 4096 x
+// 4096) 122 with one block each, 82 with the two that this gives; 128 x 128 (8 heads, 2048 x
+// 2048) 74 with one, 97 to 117 with two on either side.  What it leaves: a long axis where one set
+// ends in a short second round.  160 x 640 (10 heads, 2048 x 8192) 394, two or three
+// blocks for dQ 366; 80 x 640 (1024 x 8192) 215, three 207 (two 235).
 int split_to_fill(long long blocks, long long steps, long long slots) {
     if (blocks >= slots) return 1;
     return static_cast<int>(std::max(1LL, std::min(steps, slots / blocks)));
