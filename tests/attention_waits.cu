@@ -1,8 +1,10 @@
 // Bounded waits of the attention kernels, launched by test_attention_waits.py.
-// dK and dV of the bf16 backward pass behind a slow kernel:
-// The library launches attn_dkdv_tc_kernel beside the last blocks of the kernel that forms
-// delta; here that one is replaced by a kernel that lets its successor start at once, takes
-// as long as it is told and only then writes delta.
+//
+// dkdv_behind: dK and dV of the bf16 backward pass behind a slow kernel.  The library launches
+// attn_dkdv_tc_kernel beside the last blocks of the kernel that forms delta; here that one
+// is replaced by a kernel that lets its successor start at once, takes as long as it is
+// told and only then writes delta.
+// run_out: a wait on a barrier that nothing arrives at.
 #include "lard_host.h"
 #include "attn/attn_bwd_tc.cuh"
 
